@@ -278,7 +278,7 @@ def _plain_tables(s):
     done, held = new < 0, (ctx + page - 1) // page
     rel = torch.where(done, held, torch.zeros_like(held))
     rel_end = rel.cumsum(0)
-    rows = new.clamp(0, n_tokens)
+    rows = new.clamp(0, n_tokens + 1)
     row_end = rows.cumsum(0)
     cu = torch.cat([row_end.new_zeros(1), row_end]).clamp_max(n_tokens)
     fits = ~done & (ctx + rows <= cap) & (rows <= pad if pad else row_end <= n_tokens)
