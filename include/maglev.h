@@ -46,9 +46,10 @@ typedef enum {
   MAGLEV_ERR_UNSUPPORTED = 2,
   MAGLEV_ERR_CUDA = 3,
   MAGLEV_ERR_TIMEOUT = 4,
-  /* Only from a library built with -DMAGLEV_DEBUG (libmaglev_debug.so): an
-   * in-kernel index check failed; the access was skipped. Reported through
-   * maglev_device_status like MAGLEV_ERR_TIMEOUT. */
+  /* An in-kernel index check failed; the access was skipped. Reported through
+   * maglev_device_status like MAGLEV_ERR_TIMEOUT. The paged calls check page
+   * numbers, slots and lengths in every build; the other checks exist only in
+   * a library built with -DMAGLEV_DEBUG (libmaglev_debug.so). */
   MAGLEV_ERR_BOUNDS = 5
 } maglev_status;
 
@@ -84,6 +85,28 @@ typedef struct {
   int64_t spin_limit;
   int shared_kv_gates;
 } maglev_decode_desc;
+
+/* A paged key/value cache and the sequences that live in it. The cache of one
+ * layer is two pools k_pages, v_pages [num_pages, H_kv, page_size, hd] of
+ * `dtype`; entries are stored post-RoPE and post-mix, as in the decode rings.
+ * Row b of block_table [B, max_pages] (int32, one table for all layers) names
+ * the pages of sequence b in order: the entry of absolute position j lies in
+ * page block_table[b, j / page_size], row j % page_size; its slot number is
+ * page * page_size + row. B sequences, H query heads reading H_kv key/value
+ * heads (H % H_kv == 0; query head h reads head h / (H / H_kv)), hd 64 or 128,
+ * page_size a power of two in [16, 256], window W >= 1 (keys max(0, p-W+1)..p) or
+ * 0 (every position up to p), the other fields as in maglev_decode_desc. Gate
+ * logits are [4, H_kv] ([2, H_kv] with shared_kv_gates). page numbers, slots
+ * and lengths come from the device: one that lies outside the pool or the
+ * table is never followed, and the call records MAGLEV_ERR_BOUNDS in the device
+ * status word (in every build). */
+typedef struct {
+  int B, H, H_kv, hd, page_size, max_pages, num_pages, window;
+  float rope_base, rms_eps;
+  int inject;
+  int dtype;
+  int shared_kv_gates;
+} maglev_paged_desc;
 
 /* Library version string (static storage). */
 const char* maglev_version(void);
@@ -398,6 +421,91 @@ maglev_status maglev_decode_step(const maglev_decode_desc* desc, const int64_t* 
  * CTAs and keeps each half's partial softmax state and a per-pair counter
  * there; 0 for the fp32 path (workspace may then be NULL). */
 size_t maglev_decode_workspace_bytes(const maglev_decode_desc* desc);
+
+/* Page tables and slot maps from request lengths: one call per step of a
+ * serving loop, entirely on the device. Uses desc's B, page_size, max_pages and
+ * num_pages only (the other fields are not read).
+ * Request b holds ceil(ctx_len[b] / page_size) pages of row b.
+ *   new_len[b] >= 0: it brings that many tokens, at positions ctx_len[b]...
+ *     It is served if its row has columns for them, its token rows exist (below)
+ *     and the pages it needs are there: requests are taken in order, and one
+ *     that needs pages is served only while the pages asked for by it and the
+ *     requests before it fit into the free ones. A served request gets its
+ *     new pages from the top of the free stack (columns in order) and the
+ *     length ctx_len + new_len; another keeps its length and row.
+ *   new_len[b] < 0: it is finished. Its pages go back on the free stack (in
+ *     order of request and column) before any page is handed out; its length
+ *     becomes 0. Its row is left as it was.
+ *   n_tokens, pad: token rows. pad == 0: packed, token i of request b is row
+ *     cu_tokens[b] + i; a request whose rows end beyond n_tokens is not served.
+ *     pad >= 1: row b * pad + i, n_tokens == B * pad; one with new_len > pad is
+ *     not served.
+ *   ctx_len, new_len [B] int64; free_pages [num_pages] int32 (in/out): the free
+ *     stack, entries 0..n_free-1; n_free [1] int32 (in); block_table
+ *     [B, max_pages] int32 (in/out: only columns of newly given pages change).
+ *   seq_len [B] int64 (out, may be ctx_len itself); n_free_out [1] int32 (out,
+ *     may be n_free itself); cu_tokens [B+1] int64 (out): prefix sums of
+ *     max(new_len, 0), at most n_tokens.
+ *   pos, slots [n_tokens] int64 (out): absolute position and slot of each token
+ *     row; -1 for rows without a token and for tokens of requests not served
+ *     (the calls below skip both). May be NULL when n_tokens == 0.
+ *   workspace: maglev_page_tables_workspace_bytes(desc) bytes of scratch.
+ * Errors: INVALID_ARG (sizes, NULL or misaligned pointers, pad > 0 with n_tokens
+ * != B * pad), UNSUPPORTED (B * max_pages >= 2^31 or n_tokens > 2^31). B == 0
+ * enqueues nothing. */
+maglev_status maglev_page_tables(const maglev_paged_desc* desc, const int64_t* ctx_len, const int64_t* new_len,
+                                 int64_t n_tokens, int64_t pad, int32_t* free_pages, const int32_t* n_free,
+                                 int32_t* block_table, int64_t* seq_len, int32_t* n_free_out,
+                                 int64_t* cu_tokens, int64_t* pos, int64_t* slots, void* workspace,
+                                 void* stream);
+size_t maglev_page_tables_workspace_bytes(const maglev_paged_desc* desc);
+
+/* Writes the entries of n token rows into one layer's pages (the paged form of
+ * the mix of maglev_inject_swa_fwd and of maglev_decode_prefill): prompts, or
+ * chunks of them, of any sequences together.
+ *   slots [n] int64: destination of each row; rows with a negative slot (or
+ *     position) are skipped. Slots >= 0 must differ from one another.
+ *   pos [n] int64: absolute positions; then k_bar = RoPE_pos(k), v_bar = v, and with
+ *     desc->inject k_bar = g_kl RoPE_pos(k) + g_kr RoPE_pos(RMSNorm_head(R_k)),
+ *     v_bar = g_vl v + g_vr R_v ([rainbus] 方法步骤详情). NULL: k and v already are entries
+ *     (rows of the forward's `saved` k_bar, v_bar) and are stored as they are;
+ *     desc->inject must be 0.
+ *   k, v, R_k, R_v [n, H_kv, hd] (R_k, R_v, gate_logits: only with inject);
+ *     k_pages, v_pages (in/out): no other slot changes.
+ * Uses neither block_table nor desc's B, H, max_pages and window. n == 0 enqueues
+ * nothing. */
+maglev_status maglev_paged_write(const maglev_paged_desc* desc, int64_t n, const int64_t* slots,
+                                 const int64_t* pos, const void* k, const void* v, const void* R_k,
+                                 const void* R_v, const float* gate_logits, void* k_pages, void* v_pages,
+                                 void* stream);
+
+/* One decode step of one layer over its paged cache: maglev_decode_step for
+ * sequences of any length, with grouped key/value heads.
+ *   pos [B] int64: absolute position p of each new token; a negative one leaves
+ *     the sequence's pages untouched and writes zeros to its out.
+ *   q [B,H,hd], k, v [B,H_kv,hd]: projections of the new token, before RoPE.
+ *   krec_rot, vrec [B,H_kv,hd]: from maglev_decode_mem_project with H = H_kv
+ *     (unused without inject).
+ *   k_pages, v_pages (in/out): the new entry is written to page
+ *     block_table[b, p / page_size], row p % page_size; then the query attends
+ *     over positions max(0, p-W+1)..p (W == 0: 0..p), the new entry exactly as
+ *     stored. Columns of block_table outside those positions are not read, and
+ *     neither is a page's content outside them. Entries whose page number lies
+ *     outside the pool take no part (the new one still does, and is not stored).
+ *     The pages that new entries are written to belong to one sequence each;
+ *     others may be shared.
+ *   out [B,H,hd] (out).
+ *   workspace: maglev_paged_decode_workspace_bytes(desc) bytes of scratch,
+ *     zero-filled by the caller before its first use; every completed call
+ *     leaves its counters zero again. Calls that share a workspace must not overlap.
+ * Errors: INVALID_ARG / UNSUPPORTED for a bad desc or a NULL / misaligned
+ * pointer. A position at or beyond max_pages * page_size is treated as a negative
+ * one and recorded as MAGLEV_ERR_BOUNDS. B == 0 enqueues nothing. */
+maglev_status maglev_paged_decode_step(const maglev_paged_desc* desc, const int64_t* pos, const void* q,
+                                       const void* k, const void* v, const void* krec_rot, const void* vrec,
+                                       const float* gate_logits, const int32_t* block_table, void* k_pages,
+                                       void* v_pages, void* out, void* workspace, void* stream);
+size_t maglev_paged_decode_workspace_bytes(const maglev_paged_desc* desc);
 
 #ifdef __cplusplus
 }

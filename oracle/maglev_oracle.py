@@ -452,3 +452,115 @@ def decode_step(pos, q, k, v, krec_rot, vrec, gate_logits, k_ring, v_ring,
             e = np.exp(s - s.max())
             out[b, h] = (e / e.sum()) @ vr[b, h, live]
     return out, kr, vr
+
+
+# --------------------------------------------------------------------------
+# Paged key/value cache
+# --------------------------------------------------------------------------
+def page_tables(ctx_len, new_len, n_tokens, pad, page_size, free, block_table):
+    """Pages and token rows of one serving step, request by request.
+
+    free: the free pages, last one handed out first; block_table [B, columns].
+    A finished request (new < 0) first gives back its ceil(ctx / page_size) pages;
+    then requests in order get ceil((ctx + new) / page_size) - ceil(ctx / page_size)
+    pages while the pages asked for so far fit. Returns a dict: the table, the
+    free list, lengths, prefix sums of the token counts (at most n_tokens),
+    positions and slots of the token rows (-1 without one). Inputs are not modified.
+    """
+    table = np.array(block_table)
+    stack = [int(x) for x in free]
+    B, columns = table.shape
+    ctx = [int(c) for c in ctx_len]
+    new = [int(n) for n in new_len]
+    pages = lambda n: -(-n // page_size)
+    lens = list(ctx)
+    for b in range(B):
+        if new[b] < 0:
+            stack += [int(x) for x in table[b, :pages(ctx[b])]]
+            lens[b] = 0
+    budget, asked, rows = len(stack), 0, 0
+    cu = [0]
+    pos = np.full(n_tokens, -1, dtype=np.int64)
+    slots = np.full(n_tokens, -1, dtype=np.int64)
+    for b in range(B):
+        n = max(new[b], 0)
+        first = b * pad if pad else rows
+        rows += n
+        cu.append(min(rows, n_tokens))
+        if new[b] < 0 or ctx[b] < 0 or ctx[b] + n > columns * page_size:
+            continue
+        if n > pad if pad else rows > n_tokens:
+            continue
+        need = pages(ctx[b] + n) - pages(ctx[b])
+        asked += need
+        if need and asked > budget:
+            continue
+        for c in range(pages(ctx[b]), pages(ctx[b] + n)):
+            table[b, c] = stack.pop()
+        for i in range(n):
+            p = ctx[b] + i
+            pos[first + i] = p
+            slots[first + i] = int(table[b, p // page_size]) * page_size + p % page_size
+        lens[b] = ctx[b] + n
+    return {"block_table": table, "free": stack, "seq_len": np.array(lens), "cu_tokens": np.array(cu), "pos": pos,
+            "slots": slots}
+
+
+def paged_entries(pos, k, v, R_k, R_v, gate_logits, rope_base: float = 10000.0, eps: float = 1e-6):
+    """Entries (k_bar, v_bar) of token rows: k, v [n, H_kv, hd] at positions pos [n], with the raw memory
+    projections R_k, R_v [n, H_kv, hd] mixed in (None: no injection)."""
+    posb = np.broadcast_to(np.asarray(pos)[:, None], k.shape[:2])
+    k_loc = rope(k, posb, rope_base)
+    if R_k is None:
+        return k_loc, v
+    g = gate(gate_rows(gate_logits))[:, None, :, None]
+    return g[0] * k_loc + g[1] * rope(rmsnorm(R_k, eps), posb, rope_base), g[2] * v + g[3] * R_v
+
+
+def paged_write(slots, k_bar, v_bar, k_pages, v_pages):
+    """Entries [n, H_kv, hd] to their slots (negative: skipped). Returns new pools [pages, H_kv, page_size, hd]."""
+    kp, vp = k_pages.copy(), v_pages.copy()
+    ps = kp.shape[2]
+    for i, s in enumerate(np.asarray(slots)):
+        if s >= 0:
+            kp[s // ps, :, s % ps] = k_bar[i]
+            vp[s // ps, :, s % ps] = v_bar[i]
+    return kp, vp
+
+
+def paged_attention(pos, q, block_table, k_pages, v_pages, window: int = 0, rope_base: float = 10000.0):
+    """Attention of one query per sequence, q [B, H, hd] pre-RoPE at position pos[b], over the cached entries
+    of positions max(0, p-W+1)..p (W = 0: 0..p), the one of p included; zeros where pos < 0."""
+    B, H, hd = q.shape
+    H_kv, ps = k_pages.shape[1], k_pages.shape[2]
+    pos = np.asarray(pos, dtype=np.int64)
+    q_rot = rope(q, np.broadcast_to(np.maximum(pos, 0)[:, None], (B, H)), rope_base)
+    out = np.zeros_like(q)
+    for b in range(B):
+        p = int(pos[b])
+        if p < 0:
+            continue
+        j = np.arange(max(0, p - window + 1) if window else 0, p + 1)
+        page = block_table[b, j // ps]
+        for h in range(H):
+            hk = h // (H // H_kv)
+            s = k_pages[page, hk, j % ps] @ q_rot[b, h] / np.sqrt(hd)
+            e = np.exp(s - s.max())
+            out[b, h] = (e / e.sum()) @ v_pages[page, hk, j % ps]
+    return out
+
+
+def paged_decode_step(pos, q, k, v, krec_rot, vrec, gate_logits, block_table, k_pages, v_pages, window: int = 0,
+                      rope_base: float = 10000.0, inject: bool = True):
+    """decode_step over pages: the new entry of each sequence to its page, then paged_attention.
+    Returns (out, k_pages', v_pages'); the inputs are not modified."""
+    pos = np.asarray(pos, dtype=np.int64)
+    ps = k_pages.shape[2]
+    posb = np.broadcast_to(np.maximum(pos, 0)[:, None], k.shape[:2])
+    k_new, v_new = rope(k, posb, rope_base), v
+    if inject:
+        g = gate(gate_rows(gate_logits))[:, None, :, None]
+        k_new, v_new = g[0] * k_new + g[1] * krec_rot, g[2] * v + g[3] * vrec
+    slots = [int(block_table[b, p // ps]) * ps + p % ps if p >= 0 else -1 for b, p in enumerate(pos)]
+    kp, vp = paged_write(slots, k_new, v_new, k_pages, v_pages)
+    return paged_attention(pos, q, block_table, kp, vp, window, rope_base), kp, vp

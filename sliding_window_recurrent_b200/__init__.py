@@ -45,6 +45,13 @@ class DecodeDesc(ctypes.Structure):
                 ("shared_kv_gates", ctypes.c_int)]
 
 
+class PagedDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("H_kv", ctypes.c_int), ("hd", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("window", ctypes.c_int), ("rope_base", ctypes.c_float), ("rms_eps", ctypes.c_float),
+                ("inject", ctypes.c_int), ("dtype", ctypes.c_int), ("shared_kv_gates", ctypes.c_int)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -81,6 +88,11 @@ _SIGS = {
     "maglev_decode_step": ([ctypes.POINTER(DecodeDesc)] + [_P] * 12, _I),
     "maglev_decode_workspace_bytes": ([ctypes.POINTER(DecodeDesc)], _SZ),
     "maglev_decode_prefill": ([ctypes.POINTER(SwaDesc)] + [_P] * 4, _I),
+    "maglev_page_tables": ([ctypes.POINTER(PagedDesc), _P, _P, _I64, _I64] + [_P] * 10, _I),
+    "maglev_page_tables_workspace_bytes": ([ctypes.POINTER(PagedDesc)], _SZ),
+    "maglev_paged_write": ([ctypes.POINTER(PagedDesc), _I64] + [_P] * 10, _I),
+    "maglev_paged_decode_step": ([ctypes.POINTER(PagedDesc)] + [_P] * 13, _I),
+    "maglev_paged_decode_workspace_bytes": ([ctypes.POINTER(PagedDesc)], _SZ),
     "maglev_wait_selftest": ([_P, _I, _I64, _P], _I),
     "maglev_lm_head_workspace_bytes": ([_I64, _I, _I], _SZ),
     "maglev_lm_head_ce": ([_I64, _I, _I, _I, _F, _F] + [_P] * 8 + [_I64, _P], _I),
@@ -271,6 +283,34 @@ def maglev_decode_step(desc, pos, q, k, v, krec_rot, vrec, gate_logits, k_ring, 
 def maglev_decode_prefill(desc, saved, k_ring, v_ring, stream=None):
     _check(_lib.maglev_decode_prefill(ctypes.byref(desc), _ptr(saved), _ptr(k_ring), _ptr(v_ring),
                                       _stream(stream)))
+
+
+def maglev_page_tables_workspace_bytes(desc: PagedDesc) -> int:
+    return _lib.maglev_page_tables_workspace_bytes(ctypes.byref(desc))
+
+
+def maglev_page_tables(desc, ctx_len, new_len, n_tokens, pad, free_pages, n_free, block_table, seq_len, n_free_out,
+                       cu_tokens, pos, slots, workspace, stream=None):
+    _check(_lib.maglev_page_tables(ctypes.byref(desc), _ptr(ctx_len), _ptr(new_len), int(n_tokens), int(pad),
+                                   _ptr(free_pages), _ptr(n_free), _ptr(block_table), _ptr(seq_len),
+                                   _ptr(n_free_out), _ptr(cu_tokens), _ptr(pos), _ptr(slots), _ptr(workspace),
+                                   _stream(stream)))
+
+
+def maglev_paged_write(desc, n, slots, pos, k, v, R_k, R_v, gate_logits, k_pages, v_pages, stream=None):
+    _check(_lib.maglev_paged_write(ctypes.byref(desc), int(n), _ptr(slots), _ptr(pos), _ptr(k), _ptr(v), _ptr(R_k),
+                                   _ptr(R_v), _ptr(gate_logits), _ptr(k_pages), _ptr(v_pages), _stream(stream)))
+
+
+def maglev_paged_decode_workspace_bytes(desc: PagedDesc) -> int:
+    return _lib.maglev_paged_decode_workspace_bytes(ctypes.byref(desc))
+
+
+def maglev_paged_decode_step(desc, pos, q, k, v, krec_rot, vrec, gate_logits, block_table, k_pages, v_pages, out,
+                             workspace, stream=None):
+    _check(_lib.maglev_paged_decode_step(ctypes.byref(desc), _ptr(pos), _ptr(q), _ptr(k), _ptr(v), _ptr(krec_rot),
+                                         _ptr(vrec), _ptr(gate_logits), _ptr(block_table), _ptr(k_pages),
+                                         _ptr(v_pages), _ptr(out), _ptr(workspace), _stream(stream)))
 
 
 def maglev_lm_head_workspace_bytes(N: int, d: int, V: int) -> int:

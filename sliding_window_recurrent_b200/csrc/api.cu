@@ -939,4 +939,158 @@ maglev_status maglev_decode_step(const maglev_decode_desc* d, const int64_t* pos
   return MAGLEV_OK;
 }
 
+static maglev_status check_pages(const maglev_paged_desc* d) {
+  if (!d) return fail(MAGLEV_ERR_INVALID_ARG, "desc must not be NULL");
+  if (d->B < 0) return fail(MAGLEV_ERR_INVALID_ARG, "B must be >= 0");
+  if (d->page_size < 16 || d->page_size > 256 || (d->page_size & (d->page_size - 1)) != 0)
+    return fail(MAGLEV_ERR_UNSUPPORTED, "page_size %d unsupported (a power of two in [16, 256])", d->page_size);
+  if (d->max_pages < 1 || d->num_pages < 1)
+    return fail(MAGLEV_ERR_INVALID_ARG, "max_pages and num_pages must be >= 1");
+  if ((int64_t)d->B * d->max_pages >= (int64_t)1 << 31)
+    return fail(MAGLEV_ERR_UNSUPPORTED, "B * max_pages must be below 2^31");
+  return MAGLEV_OK;
+}
+
+static maglev_status check_paged(const maglev_paged_desc* d) {
+  maglev_status st = check_pages(d);
+  if (st != MAGLEV_OK) return st;
+  if (d->H < 1 || d->H_kv < 1) return fail(MAGLEV_ERR_INVALID_ARG, "H and H_kv must be >= 1");
+  if (d->H % d->H_kv != 0) return fail(MAGLEV_ERR_INVALID_ARG, "H (%d) must be a multiple of H_kv (%d)", d->H, d->H_kv);
+  if (d->H > 65536) return fail(MAGLEV_ERR_UNSUPPORTED, "H must be at most 65536");
+  if (d->hd != 64 && d->hd != 128)
+    return fail(MAGLEV_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d->hd);
+  if (d->window < 0) return fail(MAGLEV_ERR_INVALID_ARG, "window must be >= 0 (0: every position)");
+  if (d->dtype != MAGLEV_F32 && d->dtype != MAGLEV_BF16)
+    return fail(MAGLEV_ERR_INVALID_ARG, "dtype must be MAGLEV_F32 or MAGLEV_BF16");
+  if (!(d->rope_base > 1.0f) || !std::isfinite(d->rope_base))
+    return fail(MAGLEV_ERR_INVALID_ARG, "rope_base must be finite and > 1");
+  if (!(d->rms_eps >= 0.0f) || !std::isfinite(d->rms_eps))
+    return fail(MAGLEV_ERR_INVALID_ARG, "rms_eps must be finite and >= 0");
+  return MAGLEV_OK;
+}
+
+static PagedShape paged_shape(const maglev_paged_desc* d) {
+  PagedShape s;
+  s.B = d->B;
+  s.H = d->H;
+  s.Hkv = d->H_kv;
+  s.hd = d->hd;
+  s.page_size = d->page_size;
+  s.max_pages = d->max_pages;
+  s.num_pages = d->num_pages;
+  s.window = d->window;
+  s.inject = d->inject ? 1 : 0;
+  s.dtype = d->dtype;
+  s.vg = d->shared_kv_gates ? 0 : 2;
+  s.log2_base = std::log2((double)d->rope_base);
+  s.eps = d->rms_eps;
+  return s;
+}
+
+size_t maglev_page_tables_workspace_bytes(const maglev_paged_desc* d) {
+  if (check_pages(d) != MAGLEV_OK) return 0;
+  return page_tables_workspace_bytes(d->B);
+}
+
+maglev_status maglev_page_tables(const maglev_paged_desc* d, const int64_t* ctx_len, const int64_t* new_len,
+                                 int64_t n_tokens, int64_t pad, int32_t* free_pages, const int32_t* n_free,
+                                 int32_t* block_table, int64_t* seq_len, int32_t* n_free_out,
+                                 int64_t* cu_tokens, int64_t* pos, int64_t* slots, void* workspace,
+                                 void* stream) {
+  maglev_status st = check_pages(d);
+  if (st != MAGLEV_OK) return st;
+  if (n_tokens < 0 || pad < 0) return fail(MAGLEV_ERR_INVALID_ARG, "n_tokens and pad must be >= 0");
+  if (n_tokens > (int64_t)1 << 31) return fail(MAGLEV_ERR_UNSUPPORTED, "n_tokens must be at most 2^31");
+  if (pad > 0 && (n_tokens % pad != 0 || n_tokens / pad != d->B))
+    return fail(MAGLEV_ERR_INVALID_ARG, "n_tokens must be B * pad when pad > 0");
+  if (d->B == 0) return MAGLEV_OK;
+  NEED_PTR(ctx_len);
+  NEED_PTR(new_len);
+  NEED_PTR(free_pages);
+  NEED_PTR(n_free);
+  NEED_PTR(block_table);
+  NEED_PTR(seq_len);
+  NEED_PTR(n_free_out);
+  NEED_PTR(cu_tokens);
+  if (n_tokens > 0) {
+    NEED_PTR(pos);
+    NEED_PTR(slots);
+  }
+  NEED_PTR(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = nullptr;
+  st = status_word(&err, s);
+  if (st != MAGLEV_OK) return st;
+  const PageTablesArgs a{d->B,    d->page_size, d->max_pages, d->num_pages, n_tokens,   pad,       ctx_len, new_len,
+                         free_pages, n_free,    block_table,  seq_len,      n_free_out, cu_tokens, pos,     slots};
+  MAGLEV_LAUNCH(page_tables_kernels(n_tokens), s, launch_page_tables(a, workspace, err, s), "page_tables");
+  return MAGLEV_OK;
+}
+
+maglev_status maglev_paged_write(const maglev_paged_desc* d, int64_t n, const int64_t* slots, const int64_t* pos,
+                                 const void* k, const void* v, const void* R_k, const void* R_v,
+                                 const float* gate_logits, void* k_pages, void* v_pages, void* stream) {
+  maglev_status st = check_paged(d);
+  if (st != MAGLEV_OK) return st;
+  if (n < 0) return fail(MAGLEV_ERR_INVALID_ARG, "n must be >= 0");
+  if (n > (int64_t)1 << 31) return fail(MAGLEV_ERR_UNSUPPORTED, "n must be at most 2^31");
+  if (d->inject && !pos) return fail(MAGLEV_ERR_INVALID_ARG, "entries stored as they are (pos NULL) take no injection");
+  if (n == 0) return MAGLEV_OK;
+  NEED_PTR(slots);
+  OPT_PTR(pos);
+  NEED_PTR(k);
+  NEED_PTR(v);
+  NEED_PTR(k_pages);
+  NEED_PTR(v_pages);
+  if (d->inject) {
+    NEED_PTR(R_k);
+    NEED_PTR(R_v);
+    NEED_PTR(gate_logits);
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = nullptr;
+  st = status_word(&err, s);
+  if (st != MAGLEV_OK) return st;
+  MAGLEV_LAUNCH(1, s, launch_paged_write(paged_shape(d), n, slots, pos, k, v, R_k, R_v, gate_logits, k_pages,
+                                         v_pages, err, s),
+                "paged_write");
+  return MAGLEV_OK;
+}
+
+size_t maglev_paged_decode_workspace_bytes(const maglev_paged_desc* d) {
+  if (check_paged(d) != MAGLEV_OK) return 0;
+  return paged_decode_workspace_bytes(paged_shape(d));
+}
+
+maglev_status maglev_paged_decode_step(const maglev_paged_desc* d, const int64_t* pos, const void* q, const void* k,
+                                       const void* v, const void* krec_rot, const void* vrec,
+                                       const float* gate_logits, const int32_t* block_table, void* k_pages,
+                                       void* v_pages, void* out, void* workspace, void* stream) {
+  maglev_status st = check_paged(d);
+  if (st != MAGLEV_OK) return st;
+  if (d->B == 0) return MAGLEV_OK;
+  NEED_PTR(pos);
+  NEED_PTR(q);
+  NEED_PTR(k);
+  NEED_PTR(v);
+  NEED_PTR(block_table);
+  NEED_PTR(k_pages);
+  NEED_PTR(v_pages);
+  NEED_PTR(out);
+  if (d->inject) {
+    NEED_PTR(krec_rot);
+    NEED_PTR(vrec);
+    NEED_PTR(gate_logits);
+  }
+  if (paged_decode_workspace_bytes(paged_shape(d)) > 0) NEED_PTR(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int* err = nullptr;
+  st = status_word(&err, s);
+  if (st != MAGLEV_OK) return st;
+  MAGLEV_LAUNCH(1, s, launch_paged_decode(paged_shape(d), pos, q, k, v, krec_rot, vrec, gate_logits, block_table,
+                                          k_pages, v_pages, out, workspace, err, s),
+                "paged_decode_step");
+  return MAGLEV_OK;
+}
+
 }  // extern "C"

@@ -95,6 +95,36 @@ cudaError_t launch_decode_step(const DecShape& s, const int64_t* pos, const void
                                const float* gates, void* k_ring, void* v_ring, void* out, void* workspace,
                                int64_t limit_us, int* err, cudaStream_t st);
 
+// A layer's paged cache (maglev_paged_desc); window 0: every position up to p.
+struct PagedShape {
+  int B, H, Hkv, hd, page_size, max_pages, num_pages, window, inject, dtype;
+  int vg;  // as in SwaShape
+  double log2_base;
+  float eps;
+};
+struct PageTablesArgs {
+  int B, page_size, max_pages, num_pages;
+  int64_t n_tokens, pad;
+  const int64_t *ctx_len, *new_len;
+  int32_t* free_pages;
+  const int32_t* n_free;
+  int32_t* block_table;
+  int64_t* seq_len;
+  int32_t* n_free_out;
+  int64_t *cu_tokens, *pos, *slots;
+};
+size_t page_tables_workspace_bytes(int B);
+int page_tables_kernels(int64_t n_tokens);  // kernels that the launch below enqueues
+cudaError_t launch_page_tables(const PageTablesArgs& a, void* workspace, int* err, cudaStream_t st);
+// pos == nullptr: k, v are stored as they are.
+cudaError_t launch_paged_write(const PagedShape& s, int64_t n, const int64_t* slots, const int64_t* pos, const void* k,
+                               const void* v, const void* Rk, const void* Rv, const float* gates, void* k_pages,
+                               void* v_pages, int* err, cudaStream_t st);
+size_t paged_decode_workspace_bytes(const PagedShape& s);
+cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const void* q, const void* k, const void* v,
+                                const void* krec, const void* vrec, const float* gates, const int32_t* block_table,
+                                void* k_pages, void* v_pages, void* out, void* workspace, int* err, cudaStream_t st);
+
 // tcgen05 projection GEMMs (bf16 in/out, fp32 accumulation in TMEM).
 // R_k | R_v [M, D] = m_shift [M, d] x [W_mk; W_mv]^T. Needs d % 8 == 0, D % 256 == 0.
 cudaError_t launch_proj_fwd_tc(int64_t M, int D, int d, const void* m_shift, const void* w_mk,

@@ -7,11 +7,12 @@ from __future__ import annotations
 
 import torch
 
-from . import (DecodeDesc, MAGLEV_BF16, MAGLEV_BWD_PREPARED, MAGLEV_DR_WRITE, MAGLEV_F32, SwaDesc,
+from . import (DecodeDesc, MAGLEV_BF16, MAGLEV_BWD_PREPARED, MAGLEV_DR_WRITE, MAGLEV_F32, PagedDesc, SwaDesc,
                maglev_consistency_loss, maglev_consistency_loss_prepare_bwd, maglev_consistency_workspace_bytes, maglev_decode_mem_project, maglev_decode_step,
                maglev_decode_workspace_bytes,
-               maglev_inject_swa_bwd, maglev_inject_swa_fwd, maglev_swa_bwd_workspace_bytes,
-               maglev_swa_saved_bytes)
+               maglev_inject_swa_bwd, maglev_inject_swa_fwd, maglev_page_tables, maglev_page_tables_workspace_bytes,
+               maglev_paged_decode_step, maglev_paged_decode_workspace_bytes, maglev_paged_write,
+               maglev_swa_bwd_workspace_bytes, maglev_swa_saved_bytes)
 
 TORCH_DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
 CODE = {"bf16": MAGLEV_BF16, "f32": MAGLEV_F32}
@@ -105,4 +106,80 @@ class DecodeLayerState:
     def step(self, pos, q, k, v, gates, k_ring, v_ring, stream=None):
         maglev_decode_step(self.desc, pos, q, k, v, self.krec, self.vrec, gates, k_ring, v_ring,
                            self.out, self.workspace, stream)
+        return self.out
+
+
+def _paged_desc(tables, H, H_kv, hd, window, dtype, inject, rope_base, eps, shared_kv_gates):
+    return PagedDesc(B=tables.B, H=H, H_kv=H_kv, hd=hd, page_size=tables.page_size, max_pages=tables.max_pages,
+                     num_pages=tables.num_pages, window=window, rope_base=rope_base, rms_eps=eps, inject=int(inject),
+                     dtype=CODE[dtype], shared_kv_gates=int(shared_kv_gates))
+
+
+class PageTables:
+    """Block table, free pages and lengths of B sequences in a paged cache, shared by its layers.
+
+    step() takes the new token counts of one serving step and returns the
+    positions and slots of its token rows; all state stays on the device, so
+    that a step can be captured in a CUDA graph.
+    """
+
+    def __init__(self, B, page_size, max_pages, num_pages, max_tokens, device="cuda"):
+        self.B, self.page_size, self.max_pages, self.num_pages = B, page_size, max_pages, num_pages
+        self.max_tokens = max_tokens
+        i32, i64 = dict(dtype=torch.int32, device=device), dict(dtype=torch.int64, device=device)
+        self.block_table = torch.full((B, max_pages), -1, **i32)
+        self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)  # page 0 is handed out first
+        self.n_free = torch.full((1,), num_pages, **i32)
+        self.lengths = torch.zeros(B, **i64)
+        self.cu_tokens = torch.zeros(B + 1, **i64)
+        self.pos = torch.full((max_tokens,), -1, **i64)
+        self.slots = torch.full((max_tokens,), -1, **i64)
+        # the library call reads the sizes only
+        self.desc = _paged_desc(self, 1, 1, 64, 0, "bf16", False, 10000.0, 1e-6, False)
+        self.workspace = _bytes(maglev_page_tables_workspace_bytes(self.desc), device)
+
+    def step(self, new_len, n_tokens=None, pad=0, stream=None):
+        """new_len [B] int64 on the device: tokens each sequence brings, -1 where it is finished.
+        Returns (pos, slots) of the first n_tokens rows (packed; pad > 0: row b * pad + i)."""
+        n = self.max_tokens if n_tokens is None else n_tokens
+        if n > self.max_tokens:
+            raise ValueError(f"n_tokens {n} exceeds the {self.max_tokens} rows this table was made for")
+        maglev_page_tables(self.desc, self.lengths, new_len, n, pad, self.free_pages, self.n_free, self.block_table,
+                           self.lengths, self.n_free, self.cu_tokens, self.pos, self.slots, self.workspace, stream)
+        return self.pos[:n], self.slots[:n]
+
+
+class PagedLayerState:
+    """One layer's pages over a PageTables, and the buffers of its decode step."""
+
+    def __init__(self, tables, H, hd, H_kv=None, window=0, d_mem=0, dtype="bf16", inject=False, rope_base=10000.0,
+                 eps=1e-6, device="cuda", shared_kv_gates=False):
+        self.tables = tables
+        H_kv = H if H_kv is None else H_kv
+        self.desc = _paged_desc(tables, H, H_kv, hd, window, dtype, inject, rope_base, eps, shared_kv_gates)
+        td = TORCH_DTYPE[dtype]
+        B = tables.B
+        self.k_pages = torch.empty(tables.num_pages, H_kv, tables.page_size, hd, dtype=td, device=device)
+        self.v_pages = torch.empty_like(self.k_pages)
+        self.out = torch.empty(B, H, hd, dtype=td, device=device)
+        self.krec = torch.empty(B, H_kv, hd, dtype=td, device=device) if inject else None
+        self.vrec = torch.empty(B, H_kv, hd, dtype=td, device=device) if inject else None
+        self.mem_desc = DecodeDesc(B=B, H=H_kv, hd=hd, d_mem=d_mem, window=1, rope_base=rope_base, rms_eps=eps,
+                                   inject=int(inject), dtype=CODE[dtype], spin_limit=0,
+                                   shared_kv_gates=int(shared_kv_gates))
+        # zero-filled once; every completed step leaves its counters zero
+        self.workspace = torch.zeros(max(16, maglev_paged_decode_workspace_bytes(self.desc)), dtype=torch.uint8,
+                                     device=device)
+
+    def write(self, slots, pos, k, v, R_k=None, R_v=None, gates=None, stream=None):
+        """Entries of the token rows k, v [n, H_kv, hd] into their slots (pos None: as they are)."""
+        maglev_paged_write(self.desc, slots.numel(), slots, pos, k, v, R_k, R_v, gates, self.k_pages, self.v_pages,
+                           stream)
+
+    def mem_project(self, pos, m_prev, w_mk, w_mv, stream=None):
+        maglev_decode_mem_project(self.mem_desc, pos, m_prev, w_mk, w_mv, self.krec, self.vrec, stream)
+
+    def step(self, pos, q, k, v, gates=None, stream=None):
+        maglev_paged_decode_step(self.desc, pos, q, k, v, self.krec, self.vrec, gates, self.tables.block_table,
+                                 self.k_pages, self.v_pages, self.out, self.workspace, stream)
         return self.out

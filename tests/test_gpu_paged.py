@@ -1,0 +1,599 @@
+"""The paged cache on the GPU, through the C ABI, against the fp64 oracle.
+
+Bounds. A stored value is rounded once: at most eps/2 of itself (bf16 2^-8, fp32
+2^-24), beside fp32 arithmetic errors that are bounded term by term below (U =
+2^-24 per fp32 operation).
+  entries: each is a sum of at most four products of an input, a cosine or sine
+    (its angle rounded to fp32 in [-pi, pi]: pi U, its value 2 U), a gate (8 U) and
+    a norm factor (hd/16 + 8 additions and roundings U): 64 U times the sum of
+    the magnitudes covers it for hd <= 128.
+  attention: scores are dot products of hd terms. With q rotated in fp32 (16 U) and
+    carried in two bf16 parts (2^-16) the error of a score is at most e = (2^-16 +
+    (hd + 32) U) |q| |k| / sqrt(hd). Weights then err by a factor 1 + 2 e + 2^-16 (the
+    weights' own two parts) + 8 U, their sums over n keys by n U, all relative to the
+    largest |v|.
+The attention is checked against the pages as the call left them, so that the
+new entry's own rounding is not counted twice.
+"""
+import numpy as np
+import pytest
+
+import oracle
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from sliding_window_recurrent_b200 import build as _build
+    _build.build(quiet=True)
+    import sliding_window_recurrent_b200 as mg
+    from sliding_window_recurrent_b200.layer import PagedLayerState, PageTables
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+TD = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def host(x):
+    return x.detach().to(torch.float64).cpu().numpy()
+
+
+def normal(gen, shape, dtype):
+    return torch.randn(shape, generator=gen, device="cuda").to(TD[dtype])
+
+
+def generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def desc(dtype="bf16", **kw):
+    base = dict(B=1, H=2, H_kv=2, hd=128, page_size=16, max_pages=4, num_pages=8, window=0, rope_base=10000.0,
+                rms_eps=1e-6, inject=0, dtype=int(dtype == "bf16"), shared_kv_gates=0)
+    base.update(kw)
+    return mg.PagedDesc(**base)
+
+
+def within(got, ref, tol, name):
+    err = np.abs(got - ref)
+    assert np.isfinite(got).all(), f"{name}: non-finite values"
+    bad = err > tol
+    assert not bad.any(), f"{name}: {bad.sum()} of {bad.size} beyond the bound, worst {np.max(err / tol):.3g} of it"
+
+
+# ---------------------------------------------------------------------------
+# page tables
+# ---------------------------------------------------------------------------
+class Tables:
+    """Device copies of one step's inputs, and the call."""
+
+    def __init__(self, lens, new, n_tokens, pad, ps, free, table, pool):
+        i64 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int64, device="cuda")
+        self.B, self.columns = table.shape
+        self.lens, self.new = i64(lens), i64(new)
+        self.free = torch.full((pool,), -7, dtype=torch.int32, device="cuda")
+        self.free[:len(free)] = torch.tensor(free, dtype=torch.int32)
+        self.n_free = torch.tensor([len(free)], dtype=torch.int32, device="cuda")
+        self.table = torch.tensor(table, dtype=torch.int32, device="cuda")
+        self.seq_len, self.cu = torch.empty_like(self.lens), i64(np.zeros(self.B + 1))
+        self.n_out = torch.empty_like(self.n_free)
+        self.pos, self.slots = (torch.full((max(n_tokens, 1),), -9, dtype=torch.int64, device="cuda") for _ in range(2))
+        self.args = (n_tokens, pad)
+        self.desc = desc(B=self.B, page_size=ps, max_pages=self.columns, num_pages=pool)
+        self.ws = torch.empty(mg.maglev_page_tables_workspace_bytes(self.desc), dtype=torch.uint8, device="cuda")
+
+    def run(self, stream=None, in_place=False):
+        mg.maglev_page_tables(self.desc, self.lens, self.new, *self.args, self.free, self.n_free, self.table,
+                              self.lens if in_place else self.seq_len, self.n_free if in_place else self.n_out, self.cu,
+                              self.pos, self.slots, self.ws, stream)
+
+    def check(self, want, in_place=False):
+        torch.cuda.synchronize()
+        n = self.args[0]
+        eq = np.testing.assert_array_equal
+        eq(self.table.cpu().numpy(), want["block_table"])
+        eq((self.lens if in_place else self.seq_len).cpu().numpy(), want["seq_len"])
+        eq(self.cu.cpu().numpy(), want["cu_tokens"])
+        eq(self.pos[:n].cpu().numpy(), want["pos"])
+        eq(self.slots[:n].cpu().numpy(), want["slots"])
+        left = int((self.n_free if in_place else self.n_out).item())
+        assert left == len(want["free"])
+        eq(self.free[:left].cpu().numpy(), want["free"])
+        assert mg.maglev_device_status() == mg.MAGLEV_OK
+
+
+def draw_tables(seed, B, ps, columns, pad, mix, spare):
+    """lens, new, n_tokens, free list, table, pool of one step; spare: free pages per page asked for."""
+    r = np.random.Generator(np.random.Philox(seed))
+    cap = columns * ps
+    lens = r.integers(0, cap + 1, B)
+    new = np.ones(B, dtype=np.int64)
+    if mix:
+        new = np.where(r.random(B) < 0.5, new, r.integers(0, cap + 2, B))
+        new[r.random(B) < 0.2] = -1
+        new[r.random(B) < 0.1] = 0
+    held = -(-lens // ps)
+    asked = int(np.maximum(-(-(lens + np.maximum(new, 0)) // ps) - held, 0).sum())
+    pool = int(held.sum()) + int(asked * spare) + 3
+    order = r.permutation(pool).astype(np.int32)
+    table = np.full((B, columns), -1, dtype=np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :held[b]] = order[at:at + held[b]]
+        at += held[b]
+    n_tokens = B * pad if pad else int(np.maximum(new, 0).sum())
+    return lens, new, n_tokens, [int(x) for x in order[at:pool - 3]], table, pool
+
+
+@pytest.mark.parametrize("B,ps,columns,pad,mix,spare,extra", [
+    (1, 16, 1, 0, False, 1.0, 0), (1, 16, 3, 1, False, 1.0, 0), (64, 16, 20, 1, False, 1.0, 0), (64, 16, 20, 1, False, 0.3, 0),
+    (7, 16, 9, 0, True, 1.0, 0), (7, 64, 9, 0, True, 0.4, 13), (33, 32, 5, 50, True, 0.7, 0), (33, 256, 3, 300, True, 0.7, 0),
+    (1023, 16, 4, 0, True, 1.0, 5), (1024, 16, 4, 0, True, 0.5, 0), (1025, 16, 4, 1, True, 0.5, 0),
+    (2500, 128, 2, 0, True, 0.6, -3000), (3, 16, 700, 0, True, 1.0, 0), (5000, 16, 2, 1, False, 0.9, 0)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_page_tables(B, ps, columns, pad, mix, spare, extra, in_place):
+    """Every output equals the oracle's, for packed and padded rows, few and many requests, pages that run out,
+    rows behind the last token (extra > 0) and too few token rows (extra < 0)."""
+    lens, new, n_tokens, free, table, pool = draw_tables(B + columns, B, ps, columns, pad, mix, spare)
+    n_tokens = max(0, n_tokens + extra)
+    t = Tables(lens, new, n_tokens, pad, ps, free, table, pool)
+    t.run(in_place=in_place)
+    t.check(oracle.page_tables(lens, new, n_tokens, pad, ps, free, table), in_place)
+
+
+def test_page_tables_many_returned_pages():
+    """Finished requests give back more pages than are taken, over one and over two launches."""
+    for n_tokens in (6, 9000):
+        B, ps, columns = 40, 16, 600
+        r = np.random.Generator(np.random.Philox(n_tokens))
+        lens = r.integers(0, columns * ps // 2, B)
+        new = np.full(B, -1, dtype=np.int64)
+        new[::9] = [n_tokens // 6] * len(new[::9])
+        held = -(-lens // ps)
+        pool = int(held.sum()) + 4
+        order = r.permutation(pool).astype(np.int32)
+        table = np.full((B, columns), -1, dtype=np.int32)
+        for b in range(B):
+            table[b, :held[b]] = order[held[:b].sum():held[:b + 1].sum()]
+        free = [int(x) for x in order[pool - 4:]]
+        t = Tables(lens, new, n_tokens, 0, ps, free, table, pool)
+        t.run()
+        t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table))
+
+
+def test_page_tables_bad_lengths_and_pages():
+    """Lengths outside a row are refused; a page number outside the pool gives no slot and is recorded; a free count
+    above the pool's size is cut and recorded. (All are bounds checks of the kernel; nothing is followed.)"""
+    table = np.array([[3, -1], [1 << 30, -1], [0, 1]], dtype=np.int32)
+    t = Tables([-5, 3, 32], [1, 1, 1], 3, 0, 16, [2], table, 5)
+    t.run()
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS
+    assert t.slots.tolist() == [-1, -1, -1] and t.pos.tolist() == [-1, -1, -1]
+    assert t.seq_len.tolist() == [-5, 4, 32] and t.n_out.tolist() == [1]
+    t = Tables([0], [1 << 62], 3, 0, 16, [2], table[:1], 5)
+    t.run()
+    torch.cuda.synchronize()
+    assert t.seq_len.tolist() == [0] and t.cu.tolist() == [0, 3] and t.slots.tolist() == [-1] * 3
+    assert mg.maglev_device_status() == mg.MAGLEV_OK
+    t = Tables([0], [1], 1, 0, 16, [2], table[:1], 5)
+    t.n_free.fill_(1 << 30)
+    t.run()
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS and t.n_out.tolist() == [4]
+
+
+# ---------------------------------------------------------------------------
+# writes
+# ---------------------------------------------------------------------------
+def entry_bound(pos, k, v, R_k, R_v, gates, ref_k, ref_v, dtype, eps=1e-6):
+    """Bounds on the stored entries' errors (see the file's head)."""
+    spread = lambda x: np.abs(x) + np.abs(np.roll(x, x.shape[-1] // 2, -1))  # both channels of a pair
+    mk, mv = spread(k), np.abs(v)
+    if R_k is not None:
+        g = oracle.gate(oracle.gate_rows(gates))[:, None, :, None]
+        mk = g[0] * mk + g[1] * spread(oracle.rmsnorm(R_k, eps))
+        mv = g[2] * mv + g[3] * np.abs(R_v)
+    h = HALF[dtype]
+    return h * np.abs(ref_k) + 64 * U * mk, h * np.abs(ref_v) + 64 * U * mv
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,H_kv,ps,n", [(128, 10, 16, 1), (64, 1, 32, 5), (128, 3, 64, 333), (64, 7, 256, 1000),
+                                          (128, 2, 128, 5000), (64, 10, 16, 2369)])
+@pytest.mark.parametrize("mode", ["copy", "rope", "mix", "mix_shared"])
+def test_paged_write(dtype, hd, H_kv, ps, n, mode):
+    """Entries against the oracle within the bounds, every other slot as it was (NaN bytes included), rows with a
+    negative slot or position skipped; positions up to 2^30."""
+    gen = generator(n + hd)
+    pool = -(-n // ps) + 3
+    order = torch.randperm(pool * ps, generator=gen, device="cuda")[:n]
+    slots = torch.where(torch.rand(n, generator=gen, device="cuda") < 0.1, torch.full_like(order, -1), order)
+    if n == 1:
+        slots = order
+    pos = torch.randint(0, 1 << 30, (n,), generator=gen, device="cuda")
+    pos[::3] %= 4096
+    inject = mode.startswith("mix")
+    k, v, R_k, R_v = (normal(gen, (n, H_kv, hd), dtype) for _ in range(4))
+    gates = torch.rand(2 if mode == "mix_shared" else 4, H_kv, generator=gen, device="cuda") * 4 - 2
+    gates[1, 0] = float("-inf")
+    if n > 1 and mode != "copy":
+        pos[1] = -1
+    kp, vp = (torch.full((pool, H_kv, ps, hd), float("nan"), dtype=TD[dtype], device="cuda") for _ in range(2))
+    d = desc(dtype, H=H_kv, H_kv=H_kv, hd=hd, page_size=ps, num_pages=pool, inject=int(inject),
+             shared_kv_gates=int(mode == "mix_shared"))
+    mg.maglev_paged_write(d, n, slots, None if mode == "copy" else pos, k, v, R_k if inject else None,
+                          R_v if inject else None, gates if inject else None, kp, vp)
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_OK
+    sl = slots.cpu().numpy()
+    if mode != "copy":
+        sl = np.where(pos.cpu().numpy() < 0, -1, sl)
+    rows = np.flatnonzero(sl >= 0)
+    got_k, got_v = (host(x)[sl[rows] // ps, :, sl[rows] % ps] for x in (kp, vp))
+    if mode == "copy":
+        np.testing.assert_array_equal(got_k, host(k)[rows])
+        np.testing.assert_array_equal(got_v, host(v)[rows])
+    else:
+        p = pos.cpu().numpy()[rows]
+        rk, rv, g = (host(R_k)[rows], host(R_v)[rows], host(gates)) if inject else (None, None, None)
+        ref_k, ref_v = oracle.paged_entries(p, host(k)[rows], host(v)[rows], rk, rv, g)
+        tk, tv = entry_bound(p, host(k)[rows], host(v)[rows], rk, rv, g, ref_k, ref_v, dtype)
+        within(got_k, ref_k, tk, "k")
+        within(got_v, ref_v, tv, "v")
+    rest = np.ones((pool, ps), dtype=bool)
+    rest[sl[rows] // ps, sl[rows] % ps] = False
+    for x in (kp, vp):
+        assert torch.isnan(x.transpose(1, 2)[torch.from_numpy(rest).cuda()].float()).all()
+
+
+def test_paged_write_refuses_slots_outside_the_pool():
+    k = torch.randn(3, 2, 64, device="cuda")
+    kp, vp = torch.zeros(2, 2, 2, 16, 64, device="cuda")
+    slots = torch.tensor([32, 5, 1 << 40], device="cuda")
+    mg.maglev_paged_write(desc("f32", hd=64, num_pages=2), 3, slots, None, k, k, None, None, None, kp, vp)
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS
+    assert torch.equal(kp[0, :, 5], k[1]) and int((kp != 0).sum()) == k[1].numel()
+
+
+# ---------------------------------------------------------------------------
+# decode
+# ---------------------------------------------------------------------------
+class Step:
+    """A decode step's inputs over scattered pages; everything the step may not read is NaN or -1."""
+
+    def __init__(self, seed, pos, H, H_kv, hd, ps, window=0, inject=False, shared=False, dtype="bf16", spare=2,
+                 scale=1.0):
+        gen = generator(seed)
+        self.pos_h = np.asarray(pos, dtype=np.int64)
+        B = len(pos)
+        self.B, self.H, self.H_kv, self.hd, self.ps, self.window, self.dtype = B, H, H_kv, hd, ps, window, dtype
+        columns = int(self.pos_h.max()) // ps + 1 if B and self.pos_h.max() >= 0 else 1
+        lo = np.maximum(0, self.pos_h - window + 1) if window else np.zeros_like(self.pos_h)
+        first, count = lo // ps, np.where(self.pos_h >= 0, self.pos_h // ps - lo // ps + 1, 0)
+        pool = int(count.sum()) + spare
+        order = np.random.Generator(np.random.Philox(seed)).permutation(pool)
+        table = np.full((B, columns), -1, dtype=np.int32)
+        at = 0
+        for b in range(B):
+            table[b, first[b]:first[b] + count[b]] = order[at:at + count[b]]
+            at += count[b]
+        self.kp, self.vp = (torch.full((pool, H_kv, ps, hd), float("nan"), dtype=TD[dtype], device="cuda")
+                            for _ in range(2))
+        for b in range(B):
+            if self.pos_h[b] > lo[b]:
+                j = torch.arange(int(lo[b]), int(self.pos_h[b]))
+                page = torch.from_numpy(table[b]).long()[j // ps].cuda()
+                self.kp[page, :, (j % ps).cuda()] = normal(gen, (len(j), H_kv, hd), dtype) * scale
+                self.vp[page, :, (j % ps).cuda()] = normal(gen, (len(j), H_kv, hd), dtype)
+        self.table_h, self.table = table, torch.from_numpy(table).cuda()
+        self.pos = torch.from_numpy(self.pos_h).cuda()
+        self.q = normal(gen, (B, H, hd), dtype) * scale
+        self.k, self.v = (normal(gen, (B, H_kv, hd), dtype) for _ in range(2))
+        self.krec = self.vrec = self.gates = None
+        if inject:
+            self.krec, self.vrec = (normal(gen, (B, H_kv, hd), dtype) for _ in range(2))
+            self.gates = torch.rand(2 if shared else 4, H_kv, generator=gen, device="cuda") * 4 - 2
+        self.out = torch.full((B, H, hd), float("nan"), dtype=TD[dtype], device="cuda")
+        self.desc = desc(dtype, B=B, H=H, H_kv=H_kv, hd=hd, page_size=ps, max_pages=columns, num_pages=pool,
+                         window=window, inject=int(inject), shared_kv_gates=int(shared))
+        self.ws = torch.zeros(max(16, mg.maglev_paged_decode_workspace_bytes(self.desc)), dtype=torch.uint8,
+                              device="cuda")
+
+    def run(self, stream=None):
+        mg.maglev_paged_decode_step(self.desc, self.pos, self.q, self.k, self.v, self.krec, self.vrec, self.gates,
+                                    self.table, self.kp, self.vp, self.out, self.ws, stream)
+        return self.out
+
+    def check(self, before, status=0):
+        """Output, the written entries and every untouched byte of the pools."""
+        torch.cuda.synchronize()
+        assert mg.maglev_device_status() == status
+        bits = torch.int16 if self.dtype == "bf16" else torch.int32
+        live = np.flatnonzero(self.pos_h >= 0)
+        page = self.table_h[live, self.pos_h[live] // self.ps]
+        row = self.pos_h[live] % self.ps
+        same = torch.ones(self.kp.shape[0], self.ps, dtype=torch.bool, device="cuda")
+        same[torch.from_numpy(page).long().cuda(), torch.from_numpy(row).cuda()] = False
+        for new, old in zip((self.kp, self.vp), before):
+            assert torch.equal(new.view(bits).transpose(1, 2)[same], old.view(bits).transpose(1, 2)[same])
+        rec = (None, None, None) if self.krec is None else tuple(host(x)[live] for x in (self.krec, self.vrec)) + (
+            host(self.gates),)
+        k, v = host(self.k)[live], host(self.v)[live]
+        posb = np.broadcast_to(self.pos_h[live][:, None], k.shape[:2])
+        ref_k, ref_v = oracle.rope(k, posb, 10000.0), v
+        tk, tv = entry_bound(None, k, v, None, None, None, ref_k, ref_v, self.dtype)
+        if rec[0] is not None:
+            g = oracle.gate(oracle.gate_rows(rec[2]))[:, None, :, None]
+            mag = np.abs(k) + np.abs(np.roll(k, self.hd // 2, -1))
+            ref_k, ref_v = g[0] * ref_k + g[1] * rec[0], g[2] * v + g[3] * rec[1]
+            tk = HALF[self.dtype] * np.abs(ref_k) + 64 * U * (g[0] * mag + g[1] * np.abs(rec[0]))
+            tv = HALF[self.dtype] * np.abs(ref_v) + 64 * U * (g[2] * np.abs(v) + g[3] * np.abs(rec[1]))
+        pg, rw = torch.from_numpy(page).long().cuda(), torch.from_numpy(row).cuda()
+        if len(live):
+            within(host(self.kp[pg, :, rw]), ref_k, tk, "new k")
+            within(host(self.vp[pg, :, rw]), ref_v, tv, "new v")
+        self.check_out(live)
+
+    def check_out(self, live):
+        got = host(self.out)
+        for b in range(self.B):
+            p = int(self.pos_h[b])
+            if p < 0:
+                assert (got[b] == 0).all()
+                continue
+            lo = max(0, p - self.window + 1) if self.window else 0
+            cols = np.arange(lo // self.ps, p // self.ps + 1)
+            pages = torch.from_numpy(self.table_h[b, cols]).long().cuda()
+            kb, vb = host(self.kp[pages]), host(self.vp[pages])
+            table = np.full((1, p // self.ps + 1), -1)
+            table[0, cols] = np.arange(len(cols))
+            q = host(self.q[b:b + 1])
+            ref = oracle.paged_attention([p], q, table, kb, vb, self.window)[0]
+            j = np.arange(lo, p + 1)
+            keys, vals = kb[table[0, j // self.ps], :, j % self.ps], vb[table[0, j // self.ps], :, j % self.ps]
+            kn = np.linalg.norm(keys, axis=-1).max()
+            e = (2.0 ** -16 + (self.hd + 32) * U) * np.linalg.norm(q, axis=-1).max() * kn / np.sqrt(self.hd)
+            slack = (2 * e + 2.0 ** -16 + (8 + len(j)) * U) * np.abs(vals).max()
+            within(got[b], ref, HALF[self.dtype] * np.abs(ref) + slack, f"out of sequence {b} at {p}")
+
+
+def run_checked(s, status=0):
+    before = s.kp.clone(), s.vp.clone()
+    s.run()
+    s.check(before, status)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,H_kv,hd", [(10, 10, 128), (2, 2, 64), (8, 4, 128), (15, 3, 64), (7, 1, 128), (8, 1, 64),
+                                       (9, 1, 128), (32, 2, 64), (17, 1, 128), (40, 1, 128)])
+@pytest.mark.parametrize("ps", [16, 64])
+def test_decode_heads(dtype, H, H_kv, hd, ps):
+    """Every grouping of heads, sequences of one token to a few pages around every boundary, one not running."""
+    run_checked(Step(H + hd, [0, 1, ps - 1, -1, ps, 2 * ps + 7, 200, 333], H, H_kv, hd, ps, dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 512, 5000])
+@pytest.mark.parametrize("ps", [16, 128])
+def test_decode_windows(dtype, window, ps):
+    """Windows that begin and end anywhere in a page; pages before them are gone from the table (-1)."""
+    run_checked(Step(window, [0, 14, 15, 16, 31, 99, 100, 511, 512, 1023, 3000], 4, 2, 128, ps, window=window,
+                     dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("ps,hd", [(16, 128), (32, 64), (256, 128)])
+def test_decode_injected(dtype, shared, ps, hd):
+    """The memory mixed into the new entry, four or two gate logits per key/value head."""
+    run_checked(Step(ps, [5, 0, 700, 511, 512, -3, 64], 6, 3, hd, ps, window=512, inject=True, shared=shared,
+                     dtype=dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pos", [[20011], [9000, 3, 0, 12345], [4095] * 9, list(range(0, 2600, 13))])
+def test_decode_lengths_split_and_joined(dtype, pos):
+    """One long sequence (its keys split over many blocks), very uneven ones, many short ones."""
+    run_checked(Step(len(pos), pos, 4, 2, 128, 64, dtype=dtype))
+
+
+def test_decode_far_positions_and_large_scores():
+    """Angles at positions near 2^24 (fp32 cannot hold them), and scores of some hundreds: the running maximum has
+    to move, and most weights underflow."""
+    run_checked(Step(3, [(1 << 24) + 5, (1 << 24) - 16, 7], 2, 1, 64, 256, window=300))
+    for dtype in ("bf16", "f32"):
+        run_checked(Step(4, [900, 2000], 4, 2, 128, 16, dtype=dtype, scale=8.0))
+
+
+def test_decode_rising_scores():
+    """Keys whose scores grow along the sequence by some units a page: every tile raises the maximum."""
+    s = Step(11, [1999], 2, 1, 128, 16)
+    dirn = host(s.q)[0, 0]
+    rot = oracle.rope(dirn[None, None], np.array([[1999]]), 10000.0)[0, 0]
+    j = torch.arange(1999)
+    page = s.table[0].long().cpu()[j // 16].cuda()
+    unit = torch.from_numpy(rot / np.linalg.norm(rot)).cuda()
+    s.kp[page, 0, (j % 16).cuda()] = (unit * (j.cuda().double() / 10)[:, None]).to(torch.bfloat16)
+    run_checked(s)
+
+
+def test_decode_offsets_beyond_32_bits():
+    """Pages at the end of a pool of more than 2^31 elements."""
+    s = Step(5, [100, 31], 2, 2, 128, 256)
+    big = (1 << 31) // (2 * 256 * 128) + 40
+    kp, vp = (torch.empty(big, 2, 256, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    n = s.kp.shape[0]
+    kp[-n:], vp[-n:] = s.kp, s.vp
+    s.table_h = np.where(s.table_h >= 0, s.table_h + big - n, -1).astype(np.int32)
+    s.table = torch.from_numpy(s.table_h).cuda()
+    s.kp, s.vp, s.desc.num_pages = kp, vp, big
+    s.run()
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == 0
+    s.check_out([0, 1])
+    d = desc(H=2, page_size=256, num_pages=big)
+    slots = torch.tensor([big * 256 - 1], device="cuda")
+    k = normal(generator(1), (1, 2, 128), "bf16")
+    mg.maglev_paged_write(d, 1, slots, None, k, k, None, None, None, kp, vp)
+    torch.cuda.synchronize()
+    assert torch.equal(kp[-1, :, 255], k[0]) and torch.equal(vp[-1, :, 255], k[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_pages_outside_the_pool(dtype):
+    """Entries on pages that are not in the pool take no part and are recorded; a position beyond the table is like a
+    negative one; a new entry without a page is attended but not stored."""
+    s = Step(9, [100, 70, 40], 4, 2, 64, 16, dtype=dtype, spare=0)
+    columns = s.table_h.shape[1]
+    s.table[0, 2] = 1 << 29
+    s.table[0, 3] = -1
+    s.table[1, 70 // 16] = -1
+    s.pos[2] = columns * 16
+    before = s.kp.clone()
+    s.run()
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS
+    got = host(s.out)
+    assert (got[2] == 0).all() and np.isfinite(got).all()
+    j = np.r_[0:32, 64:101]
+    kb, vb = host(s.kp), host(s.vp)
+    q = oracle.rope(host(s.q)[:1], np.full((1, 4), 100), 10000.0)[0]
+    for h in range(4):
+        page = s.table_h[0, j // 16]
+        x = kb[page, h // 2, j % 16] @ q[h] / 8.0
+        w = np.exp(x - x.max())
+        ref = w / w.sum() @ vb[page, h // 2, j % 16]
+        within(got[0, h], ref, HALF[dtype] * np.abs(ref) + 2e-3, f"head {h}")
+    own = int(s.table_h[0, 100 // 16])
+    changed = (s.kp != before) & ~(s.kp.isnan() & before.isnan())
+    assert int(changed.any(-1).any(1).sum()) == 1 and bool(changed[own, :, 100 % 16].any())
+
+
+def test_decode_repeats_bit_for_bit_on_any_stream_and_in_a_graph():
+    """Twenty repeats on two streams and replays of a graph all give the first result's bits: the order of the joined
+    parts is fixed, and the workspace's counters are zero again after each."""
+    s = Step(21, [5000, 17, 0, 333, -1, 2048], 8, 4, 128, 16, inject=True)
+    first = s.run().clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for i in range(20):
+        s.out.fill_(float("nan"))
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side if i % 2 else torch.cuda.current_stream()):
+            s.run()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out, first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        s.run()
+    for _ in range(3):
+        s.out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(s.out, first)
+    # the graph follows positions that change under it (within the entries each sequence has)
+    s.pos_h = np.array([100, 16, 0, 0, -1, 900])
+    s.pos.copy_(torch.from_numpy(s.pos_h))
+    before = s.kp.clone(), s.vp.clone()
+    g.replay()
+    s.check(before)
+
+
+def test_workspace_may_serve_layers_of_other_shapes():
+    """One workspace, sized for the largest, for layers of different head counts and types in turn."""
+    steps = [Step(1, [700, 5], 8, 8, 128, 16), Step(2, [9000], 4, 1, 64, 32), Step(3, [64, 65, 2], 6, 2, 128, 16, dtype="f32")]
+    ws = max((s.ws for s in steps), key=torch.numel)
+    for _ in range(2):
+        for s in steps:
+            s.ws = ws
+            run_checked(s)
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,H,H_kv,window,inject", [("bf16", 10, 10, 512, True), ("bf16", 8, 2, 0, False),
+                                                        ("f32", 4, 2, 100, True)])
+def test_serving_run(dtype, H, H_kv, window, inject):
+    """Prompts, decode steps, sequences that end and new ones that take their pages, in two layers over one table:
+    every output against the oracle over its own copy of the whole history of each sequence."""
+    B, hd, ps, d_mem = 6, 128, 16, 64
+    r = np.random.Generator(np.random.Philox(H))
+    gen = generator(H)
+    T = PageTables(B, ps, 64, 120, 2048)
+    L = [PagedLayerState(T, H, hd, H_kv, window, d_mem, dtype, inject) for _ in range(2)]
+    gates = [torch.rand(4, H_kv, generator=gen, device="cuda") * 4 - 2 for _ in L] if inject else [None] * 2
+    w_mk, w_mv = (normal(gen, (H_kv * hd, d_mem), dtype) / 8 for _ in range(2))
+    lens, hist = np.zeros(B, dtype=np.int64), [[[] for _ in range(B)] for _ in L]  # stored entries
+    refused = 0
+    for it in range(14):
+        new = np.where(lens > 0, 1, r.integers(1, 400, B))
+        new[(r.random(B) < 0.2) & (lens > 0)] = -1
+        new_d = torch.from_numpy(new).cuda()
+        decode = (new == 1) & (lens > 0)
+        prompts = np.where(decode, 0, new)
+        # prompts and ends first, packed rows
+        n = int(np.maximum(prompts, 0).sum())
+        pos, slots = T.step(torch.from_numpy(prompts).cuda(), n + 3)
+        torch.cuda.synchronize()
+        seq = T.lengths.cpu().numpy()
+        cu = T.cu_tokens.cpu().numpy()
+        x = [normal(gen, (n + 3, H_kv, hd), dtype) for _ in range(4)]
+        for l, layer in enumerate(L):
+            layer.write(slots, pos, x[0], x[1], x[2] if inject else None, x[3] if inject else None, gates[l])
+        torch.cuda.synchronize()
+        for b in range(B):
+            if prompts[b] < 0:
+                for l in range(2):
+                    hist[l][b] = []
+            elif prompts[b] > 0:
+                if seq[b] != prompts[b]:
+                    refused += 1
+                    continue
+                rows = slice(int(cu[b]), int(cu[b + 1]))
+                np.testing.assert_array_equal(pos[rows].cpu().numpy(), np.arange(prompts[b]))
+                h = [host(y[rows]) for y in x]
+                for l in range(2):
+                    kb, vb = oracle.paged_entries(np.arange(prompts[b]), h[0], h[1], h[2] if inject else None,
+                                                  h[3] if inject else None, host(gates[l]) if inject else None)
+                    hist[l][b] = [(kb[i], vb[i]) for i in range(len(kb))]
+        lens = seq
+        # then one token of every running sequence
+        pos, slots = T.step(torch.from_numpy((lens > 0).astype(np.int64)).cuda(), B, 1)
+        q, k, v = normal(gen, (B, H, hd), dtype), normal(gen, (B, H_kv, hd), dtype), normal(gen, (B, H_kv, hd), dtype)
+        m = normal(gen, (B, d_mem), dtype)
+        for l, layer in enumerate(L):
+            if inject:
+                layer.mem_project(pos, m, w_mk, w_mv)
+            layer.step(pos, q, k, v, gates[l])
+        torch.cuda.synchronize()
+        assert mg.maglev_device_status() == 0
+        p_h, lens2 = pos.cpu().numpy(), T.lengths.cpu().numpy()
+        krec, vrec = (oracle.decode_mem_project(np.maximum(p_h, 0), host(m), host(w_mk), host(w_mv), H_kv)
+                      if inject else (None, None))
+        for l, layer in enumerate(L):
+            out = host(layer.out)
+            for b in range(B):
+                if p_h[b] < 0:
+                    assert (out[b] == 0).all() and lens2[b] == lens[b]
+                    continue
+                assert p_h[b] == lens[b] == len(hist[l][b]) and lens2[b] == lens[b] + 1
+                rec = (krec[b:b + 1], vrec[b:b + 1]) if inject else (None, None)
+                kb, vb = oracle.rope(host(k)[b:b + 1], np.full((1, H_kv), p_h[b]), 10000.0), host(v)[b:b + 1]
+                if inject:
+                    g = oracle.gate(host(gates[l]))[:, None, :, None]
+                    kb, vb = g[0] * kb + g[1] * rec[0], g[2] * vb + g[3] * rec[1]
+                hist[l][b].append((kb[0], vb[0]))
+                ks, vs = (np.stack([e[i] for e in hist[l][b]], 1)[None] for i in range(2))  # one page of all entries
+                ref = oracle.paged_attention([p_h[b]], host(q)[b:b + 1], np.zeros((1, 1), dtype=int), ks, vs, window)[0]
+                # stored entries, krec and vrec are off by a rounding each (2^-8 or 2^-24 of a value below ~6 gates):
+                # scores move by at most that of |q| |k| / sqrt(hd), of which a quarter is far beyond what signs leave
+                h = HALF[dtype]
+                e = 0.25 * 2 * h * np.linalg.norm(host(q)[b], axis=-1).max() * np.linalg.norm(ks, axis=-1).max() / np.sqrt(hd)
+                tol = h * np.abs(ref) + (2 * min(e, 0.5) + 2 * h + 1e-5) * np.abs(vs).max()
+                within(out[b], ref, tol, f"step {it} layer {l} sequence {b}")
+        lens = lens2
+    assert refused < 14 * B
