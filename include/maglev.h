@@ -495,9 +495,8 @@ maglev_status maglev_paged_write(const maglev_paged_desc* desc, int64_t n, const
  *     The pages that new entries are written to belong to one sequence each;
  *     others may be shared.
  *   out [B,H,hd] (out).
- *   workspace: maglev_paged_decode_workspace_bytes(desc) bytes of scratch,
- *     zero-filled by the caller before its first use; every completed call
- *     leaves its counters zero again. Calls that share a workspace must not overlap.
+ *   workspace: maglev_paged_decode_workspace_bytes(desc) bytes of scratch (any
+ *     content). Calls that share a workspace must not overlap.
  * Errors: INVALID_ARG / UNSUPPORTED for a bad desc or a NULL / misaligned
  * pointer. A position at or beyond max_pages * page_size is treated as a negative
  * one and recorded as MAGLEV_ERR_BOUNDS. B == 0 enqueues nothing. */

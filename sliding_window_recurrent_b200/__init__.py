@@ -139,10 +139,22 @@ def _ptr(x):
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    """Handle of torch's current stream on the current device. torch's own raw lookup: building a
+    torch.cuda.Stream object for it took 3 us of a 10 us call."""
+    global _current_stream
+    import torch
+    raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+
+    def _current_stream() -> int:
+        return raw(device())
+
+    return _current_stream()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -1084,12 +1084,12 @@ maglev_status maglev_paged_decode_step(const maglev_paged_desc* d, const int64_t
     NEED_PTR(vrec);
     NEED_PTR(gate_logits);
   }
-  if (paged_decode_workspace_bytes(paged_shape(d)) > 0) NEED_PTR(workspace);
+  NEED_PTR(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int* err = nullptr;
   st = status_word(&err, s);
   if (st != MAGLEV_OK) return st;
-  MAGLEV_LAUNCH(1, s, launch_paged_decode(paged_shape(d), pos, q, k, v, krec_rot, vrec, gate_logits, block_table,
+  MAGLEV_LAUNCH(2, s, launch_paged_decode(paged_shape(d), pos, q, k, v, krec_rot, vrec, gate_logits, block_table,
                                           k_pages, v_pages, out, workspace, err, s),
                 "paged_decode_step");
   return MAGLEV_OK;

@@ -14,16 +14,14 @@
 // Split. The cache is read once and nothing else is large, so the kernel is bound
 // by HBM and has to keep every SM streaming whatever the lengths are. A unit is a
 // (sequence, key/value head, group of query heads) and is cut into steps of 16
-// keys (one page holds a whole number of steps). All steps of all units, in
-// order, are dealt to the blocks of a persistent grid in equal contiguous
-// ranges: a block's range covers whole units and at most two partial ones, each
-// warp takes every NW-th step of it. A partial unit's (m, l, o) goes to the
-// workspace, and the block that completes the unit's count joins the parts in
-// block order, so results do not depend on which block came last.
-//
-// Streaming. A warp owns a ring of stages in shared memory (K and V of one step)
-// filled by its own 16-byte asynchronous copies; no block-wide barrier
-// stands between a copy and its use, and copies run ahead across units.
+// keys (a page holds a whole number of steps). All steps of all units, in order,
+// are dealt to the warps of the grid in equal contiguous ranges. A warp works
+// alone: it streams its steps through its own ring of shared-memory stages
+// (16-byte asynchronous copies that run ahead across units), keeps (m, l, o) in
+// registers, writes the outputs of units that lie in its range, and leaves parts
+// (m, l, o) of the at most two that do not in the workspace. A second kernel, whose
+// blocks are scheduled while the first one ends, joins the parts in the order of
+// the keys: the same bits whatever ran first, and no block waits for another.
 #include "paged.cuh"
 
 namespace maglev {
@@ -88,54 +86,89 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
 }
 
 // ---------------------------------------------------------------------------
-// bf16: 16 keys x up to 8 NT query heads on the tensor cores. S^T = K q^T and
-// O^T = V^T P^T take the keys (the channels) as the instruction's 16 rows and the
-// heads as its columns: with one head to a key head the heads are the side to
-// pad, and 8 columns is the least it can be padded to. The step is bound by HBM
-// (8 KB per 16 keys), which leaves room to carry q and P as two bf16 parts
-// each: S and O then are fp32-accurate and the only rounding is the output's.
+// bf16: 16 keys x some query heads on the tensor cores. S^T = K q^T and O^T = V^T P^T
+// take the keys (the channels) as the instruction's 16 rows and the heads as its
+// columns: with one head to a key head the heads are the side to pad, and 8
+// columns is the least it can be padded to. The step is bound by HBM (8 KB per 16
+// keys), which leaves room to carry q and P as two bf16 parts each: S and O then are
+// fp32-accurate and the only rounding is the output's. The 8 NT columns hold
+// both parts: up to 4 heads in one tile (columns 0-3 the upper, 4-7 the lower
+// parts), 8 and 16 heads in two and four tiles (the upper ones first).
 // ---------------------------------------------------------------------------
 template <int HD, int NT>
 struct MmaTile {
-  static constexpr int HEADS = 8 * NT, KS = HD / 16;
-  static constexpr int QROW = HD + 8;                 // padded: fragment loads hit every bank
-  static constexpr int Q_BYTES = 2 * HEADS * QROW * 2;  // upper parts, then lower parts
-  static constexpr int SCRATCH = 0;
-  float o[KS][NT][4];
-  float m[NT][2], l[NT][2];
-  uint32_t qh[KS][NT][2], ql[KS][NT][2];
+  static constexpr int HEADS = 4 * NT, KS = HD / 16;
+  static constexpr int WARP_BYTES = 0;
+  static constexpr bool ONE = NT == 1;       // both parts in one tile
+  static constexpr int NH = ONE ? 1 : NT / 2;  // tiles of scores
+  float o[KS][NH][4];
+  float m[NH][2], l[NH][2];
+  uint32_t q[KS][NT][2];
 
-  __device__ __forceinline__ static void put_q(char* qs, int j, int c, float x) {
-    bf16* q = reinterpret_cast<bf16*>(qs);
-    q[j * QROW + c] = __float2bfloat16_rn(x);
-    q[(HEADS + j) * QROW + c] = __float2bfloat16_rn(rest(x));
+  // Head of this lane's column e (of 2) in score tile n, and of its row in a B fragment.
+  __device__ __forceinline__ static int col_head(int n, int e) {
+    const int t = threadIdx.x % 4;
+    return ONE ? 2 * (t & 1) + e : 8 * n + 2 * t + e;
   }
-  __device__ __forceinline__ void begin(const char* qs) {
-    const int g = (threadIdx.x % 32) / 4, t = threadIdx.x % 4;
-    const bf16* q = reinterpret_cast<const bf16*>(qs);
+  __device__ __forceinline__ static int row_head(int n) {
+    const int g = (threadIdx.x % 32) / 4;
+    return ONE ? g & 3 : 8 * n + g;
+  }
+  // The raw q rows as B fragments; then, with the angles, rotated, scaled and split.
+  __device__ __forceinline__ void load_q(const bf16* src, int heads) {
+    const int t = threadIdx.x % 4;
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bf16* p = q + (n * 8 + g) * QROW + 16 * k + 2 * t;
+      for (int n = 0; n < NH; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          qh[k][n][e] = *reinterpret_cast<const uint32_t*>(p + 8 * e);
-          ql[k][n][e] = *reinterpret_cast<const uint32_t*>(p + HEADS * QROW + 8 * e);
+        for (int e = 0; e < 2; ++e)
+          q[k][n][e] = row_head(n) < heads
+                           ? *reinterpret_cast<const uint32_t*>(src + row_head(n) * HD + 16 * k + 8 * e + 2 * t)
+                           : 0u;
+  }
+  __device__ __forceinline__ void begin(const float2* turn, float scale, char*, int) {
+    const int t = threadIdx.x % 4;
+    const bool lower = threadIdx.x & 16;  // ONE: this lane's column holds lower parts
+#pragma unroll
+    for (int k = 0; k < KS / 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float4 w = *reinterpret_cast<const float4*>(turn + 16 * k + 8 * e + 2 * t);  // two channels' angles
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+          const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q[k][n][e]));
+          const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q[k + KS / 2][n][e]));
+          const float x0 = (a.x * w.x - b.x * w.y) * scale, x1 = (a.y * w.z - b.y * w.w) * scale;
+          const float y0 = (a.x * w.y + b.x * w.x) * scale, y1 = (a.y * w.w + b.y * w.z) * scale;
+          if (ONE) {
+            q[k][n][e] = lower ? pack2(rest(x0), rest(x1)) : pack2(x0, x1);
+            q[k + KS / 2][n][e] = lower ? pack2(rest(y0), rest(y1)) : pack2(y0, y1);
+          } else {
+            q[k][n][e] = pack2(x0, x1);
+            q[k + KS / 2][n][e] = pack2(y0, y1);
+            q[k][NT - NH + n][e] = pack2(rest(x0), rest(x1));
+            q[k + KS / 2][NT - NH + n][e] = pack2(rest(y0), rest(y1));
+          }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[k][n][e] = 0.f;
       }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+    for (int n = 0; n < NH; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][n][e] = 0.f;
+    }
   }
   // live(r): whether key r of the step takes part; all: every key does
   template <typename Live>
-  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, bool all, Live live, char*, const char*, int) {
+  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, bool all, Live live, char*, int) {
     const int lane = threadIdx.x % 32, g = lane / 4;
-    float s[NT][4], s2[NT][4];
+    float s[NH][4], s2[NH][4];  // two chains of products, short enough to hide
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NH; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
     const int kr = lane & 15;
@@ -144,23 +177,28 @@ struct MmaTile {
       uint32_t a[4];
       ldsm4(a, ks + piece<bf16, HD>(kr, 2 * k + (lane >> 4)));
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        mma16816(s[n], a, qh[k][n][0], qh[k][n][1]);
-        mma16816(s2[n], a, ql[k][n][0], ql[k][n][1]);
+      for (int n = 0; n < NH; ++n) {
+        if (ONE) {
+          mma16816(k & 1 ? s2[n] : s[n], a, q[k][n][0], q[k][n][1]);
+        } else {
+          mma16816(s[n], a, q[k][n][0], q[k][n][1]);
+          mma16816(s2[n], a, q[k][NT - NH + n][0], q[k][NT - NH + n][1]);
+        }
       }
     }
     bool grow = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NH; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         s[n][e] += s2[n][e];
+        if (ONE) s[n][e] += __shfl_xor_sync(0xffffffffu, s[n][e], 2);
         if (!all && !live(g + (e & 2) * 4)) s[n][e] = -INFINITY;
         grow |= s[n][e] > m[n][e & 1] + SLACK;
       }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NH; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float x = fmaxf(s[n][e], s[n][e + 2]);
@@ -177,9 +215,10 @@ struct MmaTile {
           }
         }
     }
-    uint32_t ph[NT][2], pl[NT][2];
+    uint32_t ph[NH][2], pl[NH][2];
+    const bool lower = threadIdx.x & 2;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NH; ++n) {
       float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -189,8 +228,12 @@ struct MmaTile {
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        ph[n][e] = transpose8x8(pack2(w[2 * e], w[2 * e + 1]));
-        pl[n][e] = transpose8x8(pack2(rest(w[2 * e]), rest(w[2 * e + 1])));
+        if (ONE) {
+          ph[n][e] = transpose8x8(lower ? pack2(rest(w[2 * e]), rest(w[2 * e + 1])) : pack2(w[2 * e], w[2 * e + 1]));
+        } else {
+          ph[n][e] = transpose8x8(pack2(w[2 * e], w[2 * e + 1]));
+          pl[n][e] = transpose8x8(pack2(rest(w[2 * e]), rest(w[2 * e + 1])));
+        }
       }
     }
     const int vr = (lane & 7) + ((lane >> 4) & 1) * 8;
@@ -199,42 +242,55 @@ struct MmaTile {
       uint32_t a[4];
       ldsm4_trans(a, vs + piece<bf16, HD>(vr, 2 * k + ((lane >> 3) & 1)));
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NH; ++n) {
         mma16816(o[k][n], a, ph[n][0], ph[n][1]);
-        mma16816(o[k][n], a, pl[n][0], pl[n][1]);
+        if (!ONE) mma16816(o[k][n], a, pl[n][0], pl[n][1]);
       }
     }
   }
-  // the warp's references and sums, then (scaled to the block's references M) its outputs
-  __device__ __forceinline__ void put_ml(float* wm, float* wl) {
-    const int lane = threadIdx.x % 32;
+  // sums over the lanes that share a head
+  __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NH; ++n) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[n][e];
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        if (lane < 4) {
-          wm[n * 8 + 2 * lane + e] = m[n][e];
-          wl[n * 8 + 2 * lane + e] = x;
-        }
+        for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+      if (ONE) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[k][n][e] += __shfl_xor_sync(0xffffffffu, o[k][n][e], 2);
       }
+    }
   }
-  template <int ROW>
-  __device__ __forceinline__ void put_o(float* wo, const float* f, int heads) {
-    const int g = (threadIdx.x % 32) / 4, t = threadIdx.x % 4;
+  // f(head, m, l) from one lane of each head
+  template <typename F>
+  __device__ __forceinline__ void each_head(int heads, F f) {
+    if (threadIdx.x % 32 < (ONE ? 2 : 4)) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NH; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (col_head(n, e) < heads) f(col_head(n, e), m[n][e], l[n][e]);
+    }
+  }
+  // f(head, channel, value * factor(l)) from the lane that holds it
+  template <typename R, typename F>
+  __device__ __forceinline__ void each_out(int heads, R factor, F f) {
+    const int g = (threadIdx.x % 32) / 4;
+    if (ONE && (threadIdx.x & 2)) return;
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = n * 8 + 2 * t + e;
+        const int j = col_head(n, e);
         if (j >= heads) continue;
-        const float a = f[j];
+        const float r = factor(l[n][e]);
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          wo[j * ROW + 16 * k + g] = o[k][n][e] * a;
-          wo[j * ROW + 16 * k + g + 8] = o[k][n][e + 2] * a;
+          f(j, 16 * k + g, o[k][n][e] * r);
+          f(j, 16 * k + g + 8, o[k][n][e + 2] * r);
         }
       }
   }
@@ -247,16 +303,36 @@ struct MmaTile {
 template <int HD>
 struct SimtTile {
   static constexpr int HEADS = 4, PIECES = HD / 4;
-  static constexpr int Q_BYTES = HEADS * HD * 4;
-  static constexpr int SCRATCH = HEADS * KSTEP * 4;  // a warp's weights of a step
+  static constexpr int WARP_BYTES = HEADS * (HD + KSTEP) * 4;  // a warp's q rows, and its weights of a step
   static constexpr int SPLIT = 32 / PIECES > 0 ? 32 / PIECES : 1;  // lanes that share a piece (hd 64: 2)
   float o[HEADS][4];
   float m[HEADS], l[HEADS];
 
-  __device__ __forceinline__ static void put_q(char* qs, int j, int c, float x) {
-    reinterpret_cast<float*>(qs)[j * HD + c] = x;
+  float q1[HEADS][HD / 64], q2[HEADS][HD / 64];
+
+  __device__ __forceinline__ void load_q(const float* q, int heads) {
+    const int lane = threadIdx.x % 32;
+#pragma unroll
+    for (int j = 0; j < HEADS; ++j)
+#pragma unroll
+      for (int r = 0; r < HD / 64; ++r) {
+        q1[j][r] = j < heads ? q[j * HD + lane + 32 * r] : 0.f;
+        q2[j][r] = j < heads ? q[j * HD + HD / 2 + lane + 32 * r] : 0.f;
+      }
   }
-  __device__ __forceinline__ void begin(const char*) {
+  __device__ __forceinline__ void begin(const float2* turn, float scale, char* room, int) {
+    const int lane = threadIdx.x % 32;
+    float* q = reinterpret_cast<float*>(room);
+#pragma unroll
+    for (int r = 0; r < HD / 64; ++r) {
+      const float2 w = turn[lane + 32 * r];
+#pragma unroll
+      for (int j = 0; j < HEADS; ++j) {
+        q[j * HD + lane + 32 * r] = (q1[j][r] * w.x - q2[j][r] * w.y) * scale;
+        q[j * HD + HD / 2 + lane + 32 * r] = (q1[j][r] * w.y + q2[j][r] * w.x) * scale;
+      }
+    }
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) {
       m[j] = -INFINITY;
@@ -271,10 +347,9 @@ struct SimtTile {
     return r;
   }
   template <typename Live>
-  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, bool all, Live live, char* scratch, const char* qs,
-                                       int heads) {
+  __device__ __forceinline__ void step(uint32_t ks, uint32_t vs, bool all, Live live, char* room, int heads) {
     const int lane = threadIdx.x % 32, r = lane & 15, half = lane >> 4;
-    const float4* q = reinterpret_cast<const float4*>(qs);
+    const float4* q = reinterpret_cast<const float4*>(room);
     float s[HEADS];
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) s[j] = 0.f;
@@ -289,7 +364,7 @@ struct SimtTile {
           s[j] = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s[j]))));
         }
     }
-    float* w = reinterpret_cast<float*>(scratch);
+    float* w = reinterpret_cast<float*>(room) + HEADS * HD;
     const bool on = all || live(r);
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) {
@@ -327,32 +402,35 @@ struct SimtTile {
         }
     }
   }
-  __device__ __forceinline__ void put_ml(float* wm, float* wl) {
+  __device__ __forceinline__ void finish() {
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) {
-      float x = l[j];
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      if (threadIdx.x % 32 == 0) {
-        wm[j] = m[j];
-        wl[j] = x;
+      for (int d = 1; d < 16; d <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+      if (SPLIT > 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] += __shfl_xor_sync(0xffffffffu, o[j][e], 16);
       }
     }
   }
-  template <int ROW>
-  __device__ __forceinline__ void put_o(float* wo, const float* f, int heads) {
+  template <typename F>
+  __device__ __forceinline__ void each_head(int heads, F f) {
+    if (threadIdx.x % 32 == 0) {
+#pragma unroll
+      for (int j = 0; j < HEADS; ++j)
+        if (j < heads) f(j, m[j], l[j]);
+    }
+  }
+  template <typename R, typename F>
+  __device__ __forceinline__ void each_out(int heads, R factor, F f) {
     const int lane = threadIdx.x % 32;
+    if (lane >= PIECES) return;
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) {
       if (j >= heads) break;
-      float x[4];
+      const float r = factor(l[j]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = o[j][e];
-        if (SPLIT > 1) x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
-        x[e] *= f[j];
-      }
-      if (lane < PIECES) *reinterpret_cast<float4*>(wo + j * ROW + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+      for (int e = 0; e < 4; ++e) f(j, 4 * lane + e, o[j][e] * r);
     }
   }
 };
@@ -364,75 +442,45 @@ struct DecodeArgs {
   const float* gates;
   const int32_t* table;
   void *kp, *vp, *out;
-  float* parts;    // [grid][2][HEADS][hd + 2]
-  int* counters;   // [B * units], zero between calls
-  int shift;       // log2 of the page size
+  float* parts;      // [warps][2][heads][PART_ROW]
+  int warps;         // of the grid
+  int shift;         // log2 of the page size
   int heads, units;  // query heads of a unit (the last may have fewer), units of a sequence
   float scale_log2;
   int* err;
 };
 
-constexpr int PART_HEADS = 16, PART_ROW = 130;  // the largest part: 16 heads of 128 channels, m and l
-constexpr int MIN_STEPS = 8;                    // fewest steps of a block's range
+constexpr int PART_M = 128, PART_ROW = 132;  // a part's row: up to 128 channels, then m and l
+constexpr int MIN_STEPS = 1;                               // fewest steps of a warp's range
 
-// A sequence's steps and the unit a global step lies in.
-struct Cursor {
-  int b, hu;         // sequence, unit within it
-  int p, lo, s0, n;  // its position, first key, first step, steps (of each unit)
-  int64_t base;      // global step of the unit's first one
+// Steps of one unit of sequence b (0: not running), its position, first key, first step.
+struct Sequence {
+  int p, lo, s0, n;
 };
+__device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeArgs& a, int b) {
+  Sequence r{0, 0, 0, 0};
+  const int64_t p = a.pos[b];
+  if (p < 0 || p >= (int64_t)s.max_pages << a.shift) return r;
+  r.p = (int)p;
+  r.lo = s.window > 0 && p >= s.window ? (int)p - s.window + 1 : 0;
+  r.s0 = r.lo / KSTEP;
+  r.n = r.p / KSTEP - r.s0 + 1;
+  return r;
+}
 
-template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
-__global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s, DecodeArgs a,
-                                                                  const __grid_constant__ RopeFreqs rf) {
-  constexpr int HALF = HD / 2, THREADS = NW * 32, HEADS = Tile::HEADS;
-  constexpr int CPR = HD * (int)sizeof(T) / 16;            // 16-byte pieces of an entry
-  constexpr int KV = KSTEP * HD * (int)sizeof(T);          // K (or V) bytes of a step
-  constexpr int OROW = HD + 4;                             // merge rows: four columns of one key row hit every bank
-  extern __shared__ __align__(128) char sm[];
-  char* qs = sm + NW * STAGES * 2 * KV;
-  T* kn = reinterpret_cast<T*>(qs + Tile::Q_BYTES);        // the new entry, as stored
-  T* vn = kn + HD;
-  float2* turn = reinterpret_cast<float2*>(vn + HD);       // angles of the current sequence's position
-  char* scratch = reinterpret_cast<char*>(turn + HALF) + (threadIdx.x / 32) * Tile::SCRATCH;
-  float* wm = reinterpret_cast<float*>(reinterpret_cast<char*>(turn + HALF) + NW * Tile::SCRATCH);  // [NW][HEADS]
-  float* wl = wm + NW * HEADS;
-  float* wo = wl + NW * HEADS;                             // [NW][heads][OROW]
-  __shared__ int64_t sums[NW];
-  __shared__ int sh_b, sh_last;
-  __shared__ int64_t sh_base;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t cap = (int64_t)s.max_pages << a.shift;
-  T* kp = static_cast<T*>(a.kp);
-  T* vp = static_cast<T*>(a.vp);
-  T* out = static_cast<T*>(a.out);
+// Where the global steps lie, from the positions alone: every block of both
+// kernels forms the same sums. Thread i covers `chunk` sequences from i * chunk.
+template <int THREADS>
+struct Plan {
+  int64_t before[THREADS + 1];  // steps (of one unit each) of the sequences before thread i's
+  int64_t sums[THREADS / 32];
+  int chunk;
 
-  // steps of sequence b (0: not running)
-  auto steps_of = [&](int b, int* pp, int* plo, int* ps0) -> int {
-    const int64_t p = a.pos[b];
-    if (p < 0 || p >= cap) return 0;
-    *pp = (int)p;
-    *plo = s.window > 0 && p >= s.window ? (int)p - s.window + 1 : 0;
-    *ps0 = *plo / KSTEP;
-    return (int)p / KSTEP - *ps0 + 1;
-  };
-
-  // sequences that are not running: zeros
-  for (int b = blockIdx.x; b < s.B; b += gridDim.x) {
-    const int64_t p = a.pos[b];
-    if (p >= 0 && p < cap) continue;
-    if (p >= cap && tid == 0) record_error(a.err, DEV_BOUNDS);
-    for (int i = tid; i < s.H * HD; i += THREADS) out[(int64_t)b * s.H * HD + i] = from_f<T>(0.f);
-  }
-
-  // this block's range of the global steps, and the sequence it begins in
-  int64_t r0, r1, per;
-  {
-    const int chunk = (s.B + THREADS - 1) / THREADS;
-    const int b0 = tid * chunk, b1 = b0 + chunk < s.B ? b0 + chunk : s.B;
-    int d0, d1, d2;
+  __device__ __forceinline__ void form(const PagedShape& s, const DecodeArgs& a) {  // ends in a barrier
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int per = (s.B + THREADS - 1) / THREADS;
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += steps_of(b, &d0, &d1, &d2);
+    for (int b = tid * per; b < (tid + 1) * per && b < s.B; ++b) mine += sequence(s, a, b).n;
     int64_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -441,250 +489,363 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     }
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    int64_t before = 0, total = 0;
+    int64_t base = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
-    }
-    total *= a.units;
-    per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < MIN_STEPS) per = MIN_STEPS;
-    per = (per + NW - 1) / NW * NW;
-    r0 = per * blockIdx.x;
-    r1 = r0 + per < total ? r0 + per : total;
-    if (r0 >= r1) return;
-    int64_t at = (before + inc - mine) * a.units;
-    if (r0 >= at && r0 < at + mine * a.units) {
-      int b = b0;
-      for (;; ++b) {
-        const int64_t n = (int64_t)steps_of(b, &d0, &d1, &d2) * a.units;
-        if (r0 < at + n) break;
-        at += n;
-      }
-      sh_b = b;
-      sh_base = at;
+    for (int w = 0; w < THREADS / 32; ++w)
+      if (w < warp) base += sums[w];
+    before[tid + 1] = base + inc;
+    if (tid == 0) {
+      before[0] = 0;
+      chunk = per;
     }
     __syncthreads();
   }
-  Cursor cur;  // the unit being worked on
-  cur.b = sh_b;
-  cur.n = steps_of(cur.b, &cur.p, &cur.lo, &cur.s0);
-  cur.hu = (int)((r0 - sh_base) / cur.n);
-  cur.base = sh_base + (int64_t)cur.hu * cur.n;
-  auto seek = [&](Cursor& c, int64_t t) {  // moves on to the unit of step t < r1
-    while (t >= c.base + c.n) {
-      c.base += c.n;
-      if (++c.hu == a.units) {
-        c.hu = 0;
-        do c.n = steps_of(++c.b, &c.p, &c.lo, &c.s0);
-        while (c.n == 0);
-      }
-    }
-  };
-  const int groups = a.units / s.Hkv;  // units of a key/value head
+  // steps of a warp's range
+  __device__ __forceinline__ int64_t range(const DecodeArgs& a) const {
+    const int64_t per = (before[THREADS] * a.units + a.warps - 1) / a.warps;
+    return per < MIN_STEPS ? MIN_STEPS : per;
+  }
+};
 
-  // ---- the warp's copies
+// The unit that a global step lies in: sequence, unit within it, its first step.
+struct Cursor {
+  int b, hu;
+  Sequence q;
+  int64_t base;
+};
+template <int THREADS>
+__device__ __forceinline__ Cursor locate(const Plan<THREADS>& plan, const PagedShape& s, const DecodeArgs& a, int64_t t) {
+  int lo = 0, hi = THREADS - 1;  // the first chunk whose steps end after t
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (plan.before[mid + 1] * a.units > t) hi = mid;
+    else lo = mid + 1;
+  }
+  Cursor c;
+  c.b = lo * plan.chunk;
+  int64_t at = plan.before[lo] * a.units;
+  for (;; ++c.b) {
+    c.q = sequence(s, a, c.b);
+    if (t < at + (int64_t)c.q.n * a.units) break;
+    at += (int64_t)c.q.n * a.units;
+  }
+  c.hu = (int)((t - at) / c.q.n);
+  c.base = at + (int64_t)c.hu * c.q.n;
+  return c;
+}
+// Moves on to the unit of a later step.
+__device__ __forceinline__ void seek(Cursor& c, const PagedShape& s, const DecodeArgs& a, int64_t t) {
+  while (t >= c.base + c.q.n) {
+    c.base += c.q.n;
+    if (++c.hu == a.units) {
+      c.hu = 0;
+      do c.q = sequence(s, a, ++c.b);
+      while (c.q.n == 0);
+    }
+  }
+}
+
+template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
+__global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s, DecodeArgs a,
+                                                                  const __grid_constant__ RopeFreqs rf) {
+  constexpr int HALF = HD / 2, NP = HALF / 32;
+  constexpr int CPR = HD * (int)sizeof(T) / 16;    // 16-byte pieces of an entry
+  constexpr int KV = KSTEP * HD * (int)sizeof(T);  // K (or V) bytes of a step
+  extern __shared__ __align__(128) char sm[];
+  __shared__ Plan<NW * 32> plan;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  char* stages = sm + warp * STAGES * 2 * KV;
+  char* after = sm + NW * STAGES * 2 * KV;
+  char* room = after + warp * Tile::WARP_BYTES;
+  T* entry = reinterpret_cast<T*>(after + NW * Tile::WARP_BYTES) + warp * 2 * HD;  // the warp's new K, V
+  float2* turn = reinterpret_cast<float2*>(after + NW * (Tile::WARP_BYTES + 2 * HD * sizeof(T))) + warp * HALF;
+  T* kp = static_cast<T*>(a.kp);
+  T* vp = static_cast<T*>(a.vp);
+  T* out = static_cast<T*>(a.out);
+
+  asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks may take the places that come free
+  plan.form(s, a);
+  const int64_t per = plan.range(a), total = plan.before[NW * 32] * a.units;
+  const int me = blockIdx.x * NW + warp;
+  const int64_t t0 = per * me, t1 = t0 + per < total ? t0 + per : total;  // the warp's range
+  if (t0 >= t1) return;
+  const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;  // units, query heads of a key/value head
+  Cursor cur = locate(plan, s, a, t0);  // the unit being worked on
+
+  // ---- copies
   Cursor ahead = cur;
-  int64_t ti = r0 + warp;  // the next step to copy
-  int page = -1;           // its page, looked up one step before it is needed
-  uint32_t bad = 0;        // stages whose page lies outside the pool
+  int64_t ti = t0;   // the next step to copy
+  int page = -1;     // its page, looked up one step before it is needed
+  uint32_t bad = 0;  // stages whose page lies outside the pool
   auto look = [&]() {
-    if (ti >= r1) return;
-    seek(ahead, ti);
-    const int key = (ahead.s0 + (int)(ti - ahead.base)) * KSTEP;
+    if (ti >= t1) return;
+    seek(ahead, s, a, ti);
+    const int key = (ahead.q.s0 + (int)(ti - ahead.base)) * KSTEP;
     page = a.table[(int64_t)ahead.b * s.max_pages + (key >> a.shift)];
   };
-  const uint32_t stage0 = smem_u32(sm) + warp * STAGES * 2 * KV;
+  const uint32_t stage0 = smem_u32(stages);
   auto issue = [&](int st) {
-    if (ti < r1) {
-      const int key = (ahead.s0 + (int)(ti - ahead.base)) * KSTEP;
+    if (ti < t1) {
+      const int key = (ahead.q.s0 + (int)(ti - ahead.base)) * KSTEP;
       const int hk = ahead.hu / groups;
       const bool ok = page >= 0 && page < s.num_pages;
       // keys [from, to) of the step lie in the cache; the new entry (position p) does not
-      const int from = ok ? ahead.lo - key : KSTEP, to = ok ? ahead.p - key : 0;
+      const int from = ok ? ahead.q.lo - key : KSTEP, to = ok ? ahead.q.p - key : 0;
       const int64_t e = ((((int64_t)(ok ? page : 0) * s.Hkv + hk) << a.shift) + (key & (s.page_size - 1))) * HD;
       const char* gk = reinterpret_cast<const char*>(kp + e);
       const char* gv = reinterpret_cast<const char*>(vp + e);
       const uint32_t dk = stage0 + st * 2 * KV, dv = dk + KV;
+      if (from <= 0 && to >= KSTEP) {
 #pragma unroll
-      for (int i = 0; i < KSTEP * CPR / 32; ++i) {
-        const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
-        const int bytes = r >= from && r < to ? 16 : 0;
-        copy16(dk + piece<T, HD>(r, c), gk + x * 16, bytes);
-        copy16(dv + piece<T, HD>(r, c), gv + x * 16, bytes);
+        for (int i = 0; i < KSTEP * CPR / 32; ++i) {
+          const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
+          copy16(dk + piece<T, HD>(r, c), gk + x * 16, 16);
+          copy16(dv + piece<T, HD>(r, c), gv + x * 16, 16);
+        }
+      } else {
+        for (int i = 0; i < KSTEP * CPR / 32; ++i) {
+          const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
+          const int bytes = r >= from && r < to ? 16 : 0;
+          copy16(dk + piece<T, HD>(r, c), gk + x * 16, bytes);
+          copy16(dv + piece<T, HD>(r, c), gv + x * 16, bytes);
+        }
       }
       bad = ok ? bad & ~(1u << st) : bad | (1u << st);
       if (!ok && lane == 0) record_error(a.err, DEV_BOUNDS);
-      ti += NW;
+      ++ti;
       look();
     }
     copy_commit();
   };
+  int turned = -1;
+  auto turn_to = [&](const Cursor& c) {  // the angles of its sequence's position
+    if (turned == c.b) return;
+    turned = c.b;
+    __syncwarp();  // the last ones have been read
+#pragma unroll
+    for (int r = 0; r < NP; ++r) turn[lane + 32 * r] = rope_turn(c.q.p, rf.turns[lane + 32 * r]);
+    __syncwarp();
+  };
   look();
+  turn_to(cur);  // while the first page number is on its way
 #pragma unroll
   for (int st = 0; st < STAGES; ++st) issue(st);
 
   // ---- the range's units in order
   Tile tile;
   int st = 0;
-  int turned = -1;
-  int64_t t = r0 + warp;  // the warp's next step to work on
-  for (int64_t at = r0; at < r1;) {
-    seek(cur, at);
-    const int64_t end = cur.base + cur.n < r1 ? cur.base + cur.n : r1;  // steps [at, end) of the unit
+  for (int64_t t = t0; t < t1;) {
+    seek(cur, s, a, t);
+    const int64_t end = cur.base + cur.q.n < t1 ? cur.base + cur.q.n : t1;  // steps [t, end) of the unit
     const int hk = cur.hu / groups;
-    const int h0 = hk * (s.H / s.Hkv) + (cur.hu % groups) * a.heads;
-    const int heads = min(a.heads, (hk + 1) * (s.H / s.Hkv) - h0);
-    const bool has_new = end == cur.base + cur.n;
-    __syncthreads();  // the last unit's q and merge rows have been read
-    if (turned != cur.b) {
-      for (int c = tid; c < HALF; c += THREADS) turn[c] = rope_turn(cur.p, rf.inv_freq[c]);
-      turned = cur.b;
-      __syncthreads();
-    }
-    for (int i = tid; i < HEADS * HALF; i += THREADS) {
-      const int j = i / HALF, c = i % HALF;
-      float x = 0.f, y = 0.f;
-      if (j < heads) {
-        const T* q = static_cast<const T*>(a.q) + ((int64_t)cur.b * s.H + h0 + j) * HD;
-        const float q1 = to_f(q[c]), q2 = to_f(q[c + HALF]);
-        const float2 w = turn[c];
-        x = (q1 * w.x - q2 * w.y) * a.scale_log2;
-        y = (q1 * w.y + q2 * w.x) * a.scale_log2;
-      }
-      Tile::put_q(qs, j, c, x);
-      Tile::put_q(qs, j, c + HALF, y);
-    }
+    const int h0 = hk * per_kv + (cur.hu % groups) * a.heads;
+    const int heads = min(a.heads, (hk + 1) * per_kv - h0);
+    const bool has_new = end == cur.base + cur.q.n, whole = t == cur.base && has_new, first = t == t0;
+    // every load of the unit at once: the query rows, and the new entry's parts
+    const int64_t row = ((int64_t)cur.b * s.Hkv + hk) * HD;
+    float k1[NP], k2[NP], v1[NP], v2[NP], kr1[NP], kr2[NP], vr1[NP], vr2[NP], ga = 0.f, gb = 0.f, gc = 0.f, gd = 0.f;
+    int pg = -1;
+    tile.load_q(static_cast<const T*>(a.q) + ((int64_t)cur.b * s.H + h0) * HD, heads);
     if (has_new) {
-      const int64_t row = ((int64_t)cur.b * s.Hkv + hk) * HD;
-      int pg = -1;
-      if (cur.hu % groups == 0) pg = a.table[(int64_t)cur.b * s.max_pages + (cur.p >> a.shift)];
-      const bool store = pg >= 0 && pg < s.num_pages;  // a bad page is recorded where its step is copied
-      const int64_t e = ((((int64_t)(store ? pg : 0) * s.Hkv + hk) << a.shift) + (cur.p & (s.page_size - 1))) * HD;
-      for (int c = tid; c < HALF; c += THREADS) {
-        const float2 w = turn[c];
-        const T *k = static_cast<const T*>(a.k) + row, *v = static_cast<const T*>(a.v) + row;
-        const float k1 = to_f(k[c]), k2 = to_f(k[c + HALF]);
-        float a1 = k1 * w.x - k2 * w.y, a2 = k1 * w.y + k2 * w.x;
-        float v1 = to_f(v[c]), v2 = to_f(v[c + HALF]);
+      const T *k = static_cast<const T*>(a.k) + row, *v = static_cast<const T*>(a.v) + row;
+      const T *kr = static_cast<const T*>(a.krec) + row, *vr = static_cast<const T*>(a.vrec) + row;
+      if (cur.hu % groups == 0) pg = a.table[(int64_t)cur.b * s.max_pages + (cur.q.p >> a.shift)];
+#pragma unroll
+      for (int r = 0; r < NP; ++r) {
+        const int c = lane + 32 * r;
+        k1[r] = to_f(k[c]);
+        k2[r] = to_f(k[c + HALF]);
+        v1[r] = to_f(v[c]);
+        v2[r] = to_f(v[c + HALF]);
         if (s.inject) {
-          const T *kr = static_cast<const T*>(a.krec) + row, *vr = static_cast<const T*>(a.vrec) + row;
-          const float gkl = gate_value(a.gates[hk]), gkr = gate_value(a.gates[s.Hkv + hk]);
-          const float gvl = gate_value(a.gates[s.vg * s.Hkv + hk]), gvr = gate_value(a.gates[(s.vg + 1) * s.Hkv + hk]);
-          a1 = gkl * a1 + gkr * to_f(kr[c]);
-          a2 = gkl * a2 + gkr * to_f(kr[c + HALF]);
-          v1 = gvl * v1 + gvr * to_f(vr[c]);
-          v2 = gvl * v2 + gvr * to_f(vr[c + HALF]);
-        }
-        kn[c] = from_f<T>(a1);  // the step attends to exactly what it stores
-        kn[c + HALF] = from_f<T>(a2);
-        vn[c] = from_f<T>(v1);
-        vn[c + HALF] = from_f<T>(v2);
-        if (store) {
-          kp[e + c] = from_f<T>(a1);
-          kp[e + c + HALF] = from_f<T>(a2);
-          vp[e + c] = from_f<T>(v1);
-          vp[e + c + HALF] = from_f<T>(v2);
+          kr1[r] = to_f(kr[c]);
+          kr2[r] = to_f(kr[c + HALF]);
+          vr1[r] = to_f(vr[c]);
+          vr2[r] = to_f(vr[c + HALF]);
         }
       }
+      if (s.inject) {
+        ga = a.gates[hk];
+        gb = a.gates[s.Hkv + hk];
+        gc = a.gates[s.vg * s.Hkv + hk];
+        gd = a.gates[(s.vg + 1) * s.Hkv + hk];
+      }
     }
-    __syncthreads();
-    tile.begin(qs);
-    for (; t < end; t += NW) {
-      const int key = (cur.s0 + (int)(t - cur.base)) * KSTEP;
+    turn_to(cur);
+    tile.begin(turn, a.scale_log2, room, heads);
+    if (has_new) {
+      const bool store = pg >= 0 && pg < s.num_pages;  // a bad page is recorded where its step is copied
+      const int64_t e = ((((int64_t)(store ? pg : 0) * s.Hkv + hk) << a.shift) + (cur.q.p & (s.page_size - 1))) * HD;
+#pragma unroll
+      for (int r = 0; r < NP; ++r) {
+        const int c = lane + 32 * r;
+        const float2 w = turn[c];
+        float x1 = k1[r] * w.x - k2[r] * w.y, x2 = k1[r] * w.y + k2[r] * w.x, y1 = v1[r], y2 = v2[r];
+        if (s.inject) {
+          const float gkl = gate_value(ga), gkr = gate_value(gb), gvl = gate_value(gc), gvr = gate_value(gd);
+          x1 = gkl * x1 + gkr * kr1[r];
+          x2 = gkl * x2 + gkr * kr2[r];
+          y1 = gvl * y1 + gvr * vr1[r];
+          y2 = gvl * y2 + gvr * vr2[r];
+        }
+        const T e1 = from_f<T>(x1), e2 = from_f<T>(x2), f1 = from_f<T>(y1), f2 = from_f<T>(y2);
+        entry[c] = e1;  // the step attends to exactly what it stores
+        entry[c + HALF] = e2;
+        entry[HD + c] = f1;
+        entry[HD + c + HALF] = f2;
+        if (store) {
+          kp[e + c] = e1;
+          kp[e + c + HALF] = e2;
+          vp[e + c] = f1;
+          vp[e + c + HALF] = f2;
+        }
+      }
+      __syncwarp();
+    }
+    for (; t < end; ++t) {
+      const int key = (cur.q.s0 + (int)(t - cur.base)) * KSTEP;
       const uint32_t ks = stage0 + st * 2 * KV, vs = ks + KV;
       copy_wait<STAGES - 1>();
       __syncwarp();
-      const int from = cur.lo - key, to = cur.p - key;  // keys [from, to] take part
+      const int from = cur.q.lo - key, to = cur.q.p - key;  // keys [from, to] take part
       const bool gone = bad >> st & 1;
       if (to < KSTEP) {  // the new entry goes where its page holds it
-        char* row = sm + (ks - smem_u32(sm));
+        char* dst = stages + st * 2 * KV;
         for (int c = lane; c < CPR; c += 32) {
-          *reinterpret_cast<uint4*>(row + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(kn)[c];
-          *reinterpret_cast<uint4*>(row + KV + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(vn)[c];
+          *reinterpret_cast<uint4*>(dst + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(entry)[c];
+          *reinterpret_cast<uint4*>(dst + KV + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(entry + HD)[c];
         }
         __syncwarp();
       }
       tile.step(
           ks, vs, from <= 0 && to >= KSTEP - 1 && !gone,
-          [&](int r) { return r == to || (!gone && r >= from && r < to); }, scratch, qs, heads);
+          [&](int r) { return r == to || (!gone && r >= from && r < to); }, room, heads);
       __syncwarp();  // every lane has read the stage
       issue(st);
       st = st + 1 == STAGES ? 0 : st + 1;
     }
-    // the warps' parts to one
-    tile.put_ml(wm + warp * HEADS, wl + warp * HEADS);
-    __syncthreads();
-    float* f = wl + NW * HEADS + NW * a.heads * OROW + warp * HEADS;  // the warp's factors
-    if (lane < heads) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * HEADS + lane]);
-      const float mine = wm[warp * HEADS + lane];
-      f[lane] = mine == -INFINITY ? 0.f : pow2(mine - M);
+    tile.finish();
+    if (whole) {
+      T* d = out + ((int64_t)cur.b * s.H + h0) * HD;
+      tile.each_out(
+          heads, [](float l) { return l == 0.f ? 0.f : 1.f / l; },
+          [&](int j, int c, float x) { d[j * HD + c] = from_f<T>(x); });
+    } else {
+      float* part = a.parts + ((int64_t)me * 2 + (first ? 0 : 1)) * a.heads * PART_ROW;
+      tile.each_out(
+          heads, [](float) { return 1.f; }, [&](int j, int c, float x) { part[j * PART_ROW + c] = x; });
+      tile.each_head(heads, [&](int j, float m, float l) {
+        *reinterpret_cast<float2*>(part + j * PART_ROW + PART_M) = make_float2(m, l);
+      });
     }
-    __syncwarp();
-    tile.template put_o<OROW>(wo + warp * a.heads * OROW, f, heads);
-    __syncthreads();
-    const bool whole = at == cur.base && has_new;
-    const float* fac = wl + NW * HEADS + NW * a.heads * OROW;
-    float* part = a.parts + ((int64_t)blockIdx.x * 2 + (at == r0 ? 0 : 1)) * PART_HEADS * PART_ROW;
-    for (int i = tid; i < heads * HD; i += THREADS) {
-      const int j = i / HD, c = i % HD;
-      float O = 0.f, L = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        O += wo[(w * a.heads + j) * OROW + c];
-        L += wl[w * HEADS + j] * fac[w * HEADS + j];
-      }
-      if (whole) {
-        out[((int64_t)cur.b * s.H + h0 + j) * HD + c] = from_f<T>(L > 0.f || L != L ? O / L : 0.f);
-      } else {
-        part[j * PART_ROW + 2 + c] = O;
-        if (c == 0) {
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * HEADS + j]);
-          part[j * PART_ROW] = M;
-          part[j * PART_ROW + 1] = L;
-        }
-      }
-    }
-    if (!whole) {
-      const int c0 = (int)(cur.base / per), c1 = (int)((cur.base + cur.n - 1) / per);  // blocks with a part
-      int* counter = a.counters + (int64_t)cur.b * a.units + cur.hu;
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();  // the block's part before its count (the fence is cumulative over the barrier)
-        sh_last = atomicAdd(counter, 1) == c1 - c0;
-        if (sh_last) {
-          __threadfence();
-          *counter = 0;  // ready for the next call
-        }
-      }
-      __syncthreads();
-      if (sh_last) {
-        auto part_of = [&](int c) {  // block c's part of this unit
-          return a.parts + ((int64_t)c * 2 + (per * c >= cur.base ? 0 : 1)) * PART_HEADS * PART_ROW;
-        };
-        for (int i = tid; i < heads * HD; i += THREADS) {
-          const int j = i / HD, c = i % HD;
-          float M = -INFINITY, L = 0.f, O = 0.f;
-          for (int x = c0; x <= c1; ++x) M = fmaxf(M, __ldcg(part_of(x) + j * PART_ROW));
-          for (int x = c0; x <= c1; ++x) {
-            const float* pr = part_of(x) + j * PART_ROW;
-            const float mx = __ldcg(pr);
-            const float w = mx == -INFINITY ? 0.f : pow2(mx - M);
-            L += w * __ldcg(pr + 1);
-            O += w * __ldcg(pr + 2 + c);
-          }
-          out[((int64_t)cur.b * s.H + h0 + j) * HD + c] = from_f<T>(L > 0.f || L != L ? O / L : 0.f);
-        }
-      }
-    }
-    at = end;
   }
+}
+
+// ---------------------------------------------------------------------------
+// The outputs of units in several warps' ranges, and zeros for sequences that are
+// not running. JW warps take a (sequence, query head) together: a lane owns four
+// channels, the warps deal the parts among them, and sixteen loads a lane are in
+// flight (what counts is the latency of parts that lie in L2).
+// ---------------------------------------------------------------------------
+constexpr int JOIN_THREADS = 256;
+
+template <typename T, int HD, int JW>
+__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedShape s, DecodeArgs a) {
+  constexpr int NW = JOIN_THREADS / 32, V = HD / 4, LANES = 32 / V;  // lanes that share four channels (hd 64: 2)
+  __shared__ Plan<JOIN_THREADS> plan;
+  __shared__ float4 so[NW][V];
+  __shared__ float sm[NW], sl[NW];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  plan.form(s, a);  // reads nothing that the first kernel writes
+  const int64_t pair = (int64_t)blockIdx.x * (NW / JW) + warp / JW;
+  const bool in = pair < (int64_t)s.B * s.H;
+  const int b = in ? (int)(pair / s.H) : 0, h = in ? (int)(pair % s.H) : 0;
+  const Sequence q = sequence(s, a, b);
+  const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
+  const int hk = h / per_kv, in_kv = h - hk * per_kv, j = in_kv % a.heads;
+  const int i = b / plan.chunk;
+  int64_t base = plan.before[i];
+  for (int x = i * plan.chunk; x < b; ++x) base += sequence(s, a, x).n;
+  base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.n;  // the unit's first step
+  const int64_t per = plan.range(a);
+  const int w0 = (int)(base / per), np = q.n ? (int)((base + q.n - 1) / per) - w0 + 1 : 0;  // warps with a part
+  const int64_t stride = (int64_t)2 * a.heads * PART_ROW;
+  // warp w0's part may follow other units in its range; the others begin with this unit
+  const float* part = a.parts + w0 * stride + j * PART_ROW;
+  auto part_of = [&](int x) { return part + x * stride + (x == 0 && base > per * w0 ? stride / 2 : 0); };
+  T* out = static_cast<T*>(a.out) + pair * HD;
+  const int c = lane % V * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (np > 1) {
+    const int step = JW * LANES, x1 = (warp % JW) * LANES + lane / V;
+#pragma unroll 1
+    for (int x0 = x1; x0 < np; x0 += 16 * step) {
+      float2 ml[16];
+      float4 y[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int x = x0 + u * step;
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (x < np) {
+          ml[u] = __ldcg(reinterpret_cast<const float2*>(part_of(x) + PART_M));
+          y[u] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + c));
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) mn = fmaxf(mn, ml[u].x);
+      const float r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r);
+      l *= f;
+      o.x *= f;
+      o.y *= f;
+      o.z *= f;
+      o.w *= f;
+      m = mn;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        if (x0 + u * step >= np) break;
+        const float w = pow2(ml[u].x - r);
+        l += w * ml[u].y;
+        o.x += w * y[u].x;
+        o.y += w * y[u].y;
+        o.z += w * y[u].z;
+        o.w += w * y[u].w;
+      }
+    }
+  }
+  auto add = [&](float m2, float l2, float4 o2) {  // another set of parts
+    const float mn = fmaxf(m, m2), r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r), f2 = pow2(m2 - r);
+    l = l * f + l2 * f2;
+    o.x = o.x * f + o2.x * f2;
+    o.y = o.y * f + o2.y * f2;
+    o.z = o.z * f + o2.z * f2;
+    o.w = o.w * f + o2.w * f2;
+    m = mn;
+  };
+  if (LANES > 1) {
+    const float4 y = make_float4(__shfl_down_sync(0xffffffffu, o.x, 16), __shfl_down_sync(0xffffffffu, o.y, 16),
+                                 __shfl_down_sync(0xffffffffu, o.z, 16), __shfl_down_sync(0xffffffffu, o.w, 16));
+    add(__shfl_down_sync(0xffffffffu, m, 16), __shfl_down_sync(0xffffffffu, l, 16), y);
+  }
+  if (JW > 1) {
+    if (lane < V) so[warp][lane] = o;
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+    __syncthreads();
+    if (warp % JW == 0 && lane < V)
+      for (int w = 1; w < JW; ++w) add(sm[warp + w], sl[warp + w], so[warp + w][lane]);
+  }
+  if (!in || np == 1 || warp % JW != 0 || lane >= V) return;  // np == 1: its warp has written it
+  if (np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  out[c] = from_f<T>(o.x * f);
+  out[c + 1] = from_f<T>(o.y * f);
+  out[c + 2] = from_f<T>(o.z * f);
+  out[c + 3] = from_f<T>(o.w * f);
 }
 
 int units_of(const PagedShape& s, int heads) {  // units of a sequence
@@ -694,39 +855,55 @@ int units_of(const PagedShape& s, int heads) {  // units of a sequence
 // Query heads of a unit: as many of a key/value head's as a tile takes.
 int tile_heads(const PagedShape& s) {
   if (s.dtype == 0) return 4;
-  return s.H / s.Hkv > 8 ? 16 : 8;
+  return s.H / s.Hkv > 8 ? 16 : s.H / s.Hkv > 4 ? 8 : 4;
 }
-constexpr int MAX_OCC = 3;  // resident blocks per SM, at most
-size_t parts_bytes() { return (size_t)num_sms() * MAX_OCC * 2 * PART_HEADS * PART_ROW * sizeof(float); }
+constexpr int MAX_WARPS = 12;  // of an SM
 
 template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
 cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
+  static_assert(NW * OCC <= MAX_WARPS, "the workspace holds the parts of MAX_WARPS warps an SM");
   const int group = s.H / s.Hkv;
   a.heads = group < Tile::HEADS ? group : Tile::HEADS;
   a.units = units_of(s, Tile::HEADS);
-  const size_t smem = (size_t)NW * STAGES * 2 * KSTEP * HD * sizeof(T) + Tile::Q_BYTES + 2 * HD * sizeof(T) +
-                      HD / 2 * sizeof(float2) + NW * Tile::SCRATCH + 3 * NW * Tile::HEADS * sizeof(float) +
-                      (size_t)NW * a.heads * (HD + 4) * sizeof(float);
-  auto kern = paged_decode_kernel<T, HD, Tile, NW, STAGES, OCC>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int occ = (int)(227 * 1024 / (smem + 1024)) < OCC ? (int)(227 * 1024 / (smem + 1024)) : OCC;
   // steps there can be at most, from the sizes alone
   int64_t keys = (int64_t)s.max_pages * s.page_size;
   if (s.window > 0 && s.window + KSTEP < keys) keys = s.window + KSTEP;
   const int64_t steps = (keys + KSTEP - 1) / KSTEP * a.units * s.B;
-  int64_t grid = (int64_t)num_sms() * occ;
-  if (grid > (steps + MIN_STEPS - 1) / MIN_STEPS) grid = (steps + MIN_STEPS - 1) / MIN_STEPS;
+  const int64_t most = (steps + NW * MIN_STEPS - 1) / (NW * MIN_STEPS);
+  constexpr size_t smem = (size_t)NW * (STAGES * 2 * KSTEP * HD * sizeof(T) + Tile::WARP_BYTES + 2 * HD * sizeof(T) +
+                                        HD / 2 * sizeof(float2));
+  static_assert((smem + sizeof(Plan<NW * 32>) + 1024) * OCC <= 228 * 1024, "OCC blocks share an SM's memory");
+  auto kern = paged_decode_kernel<T, HD, Tile, NW, STAGES, OCC>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  int64_t grid = (int64_t)num_sms() * OCC;
+  if (grid > most) grid = most;
+  a.warps = (int)grid * NW;
   kern<<<(unsigned)grid, NW * 32, smem, st>>>(s, a, rope_freqs(HD, s.log2_base));
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join: scheduled as the first kernel ends, its blocks wait for that before they read a part
+  const int64_t pairs = (int64_t)s.B * s.H;
+  const bool many = (int64_t)s.B * a.units * 4 >= a.warps;  // a few parts to a unit: a warp joins them alone
+  const int per_block = JOIN_THREADS / 32 / (many ? 1 : 8);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((pairs + per_block - 1) / per_block));
+  cfg.blockDim = dim3(JOIN_THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return many ? cudaLaunchKernelEx(&cfg, paged_join_kernel<T, HD, 1>, s, a)
+              : cudaLaunchKernelEx(&cfg, paged_join_kernel<T, HD, 8>, s, a);
 }
 
 }  // namespace
 
-// The parts have the same size for every shape, so that calls of different
-// shapes can use one workspace in turn: the counters behind them stay zero.
 size_t paged_decode_workspace_bytes(const PagedShape& s) {
-  return parts_bytes() + (size_t)s.B * units_of(s, tile_heads(s)) * sizeof(int);
+  const int group = s.H / s.Hkv, most = tile_heads(s);
+  return (size_t)num_sms() * MAX_WARPS * 2 * (group < most ? group : most) * PART_ROW * sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const void* q, const void* k, const void* v,
@@ -745,17 +922,20 @@ cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const v
   a.vp = v_pages;
   a.out = out;
   a.parts = static_cast<float*>(workspace);
-  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + parts_bytes());
   a.shift = log2_of(s.page_size);
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)s.hd);
   a.err = err;
-  const bool wide = tile_heads(s) == 16;
+  const int heads = tile_heads(s);
   if (s.dtype == 1 && s.hd == 128)
-    return wide ? run<bf16, 128, MmaTile<128, 2>, 4, 2, 2>(s, a, st) : run<bf16, 128, MmaTile<128, 1>, 4, 2, 3>(s, a, st);
+    return heads == 4   ? run<bf16, 128, MmaTile<128, 1>, 4, 2, 2>(s, a, st)
+           : heads == 8 ? run<bf16, 128, MmaTile<128, 2>, 4, 2, 2>(s, a, st)
+                        : run<bf16, 128, MmaTile<128, 4>, 4, 2, 2>(s, a, st);
   if (s.dtype == 1 && s.hd == 64)
-    return wide ? run<bf16, 64, MmaTile<64, 2>, 4, 4, 2>(s, a, st) : run<bf16, 64, MmaTile<64, 1>, 4, 4, 3>(s, a, st);
+    return heads == 4   ? run<bf16, 64, MmaTile<64, 1>, 4, 4, 3>(s, a, st)
+           : heads == 8 ? run<bf16, 64, MmaTile<64, 2>, 4, 4, 3>(s, a, st)
+                        : run<bf16, 64, MmaTile<64, 4>, 4, 4, 2>(s, a, st);
   if (s.dtype == 0 && s.hd == 128) return run<float, 128, SimtTile<128>, 4, 2, 1>(s, a, st);
-  if (s.dtype == 0 && s.hd == 64) return run<float, 64, SimtTile<64>, 4, 2, 3>(s, a, st);
+  if (s.dtype == 0 && s.hd == 64) return run<float, 64, SimtTile<64>, 4, 2, 2>(s, a, st);
   return cudaErrorInvalidValue;
 }
 

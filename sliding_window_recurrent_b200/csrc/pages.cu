@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(WRITE_THREADS) paged_write_kernel(
   const int ntok = (int)(n - t0 < tile ? n - t0 : tile);
   if (MODE != WRITE_COPY) {
     for (int i = threadIdx.x; i < ntok * HALF; i += WRITE_THREADS)
-      turn[i] = rope_turn(pos[t0 + i / HALF], rf.inv_freq[i % HALF]);
+      turn[i] = rope_turn(pos[t0 + i / HALF], rf.turns[i % HALF]);
     __syncthreads();
   }
   const int64_t nslots = (int64_t)s.num_pages << shift;

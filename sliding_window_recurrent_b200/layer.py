@@ -167,9 +167,7 @@ class PagedLayerState:
         self.mem_desc = DecodeDesc(B=B, H=H_kv, hd=hd, d_mem=d_mem, window=1, rope_base=rope_base, rms_eps=eps,
                                    inject=int(inject), dtype=CODE[dtype], spin_limit=0,
                                    shared_kv_gates=int(shared_kv_gates))
-        # zero-filled once; every completed step leaves its counters zero
-        self.workspace = torch.zeros(max(16, maglev_paged_decode_workspace_bytes(self.desc)), dtype=torch.uint8,
-                                     device=device)
+        self.workspace = _bytes(maglev_paged_decode_workspace_bytes(self.desc), device)
 
     def write(self, slots, pos, k, v, R_k=None, R_v=None, gates=None, stream=None):
         """Entries of the token rows k, v [n, H_kv, hd] into their slots (pos None: as they are)."""
