@@ -1002,7 +1002,7 @@ maglev_status maglev_page_tables(const maglev_paged_desc* d, const int64_t* ctx_
   maglev_status st = check_pages(d);
   if (st != MAGLEV_OK) return st;
   if (n_tokens < 0 || pad < 0) return fail(MAGLEV_ERR_INVALID_ARG, "n_tokens and pad must be >= 0");
-  if (n_tokens > (int64_t)1 << 31) return fail(MAGLEV_ERR_UNSUPPORTED, "n_tokens must be at most 2^31");
+  if (n_tokens > (int64_t)1 << 30) return fail(MAGLEV_ERR_UNSUPPORTED, "n_tokens must be at most 2^30");
   if (pad > 0 && (n_tokens % pad != 0 || n_tokens / pad != d->B))
     return fail(MAGLEV_ERR_INVALID_ARG, "n_tokens must be B * pad when pad > 0");
   if (d->B == 0) return MAGLEV_OK;

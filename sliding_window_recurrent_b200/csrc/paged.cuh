@@ -43,4 +43,20 @@ inline int log2_of(int x) {  // of a power of two
   return n;
 }
 
+// Launches a kernel whose blocks may be scheduled before the last launch on the
+// stream has ended; it waits for that (griddepcontrol.wait) before it reads its results.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), unsigned blocks, unsigned threads, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, Params(args)...);
+}
+
 }  // namespace maglev

@@ -886,17 +886,9 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   const int64_t pairs = (int64_t)s.B * s.H;
   const bool many = (int64_t)s.B * a.units * 4 >= a.warps;  // a few parts to a unit: a warp joins them alone
   const int per_block = JOIN_THREADS / 32 / (many ? 1 : 8);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((pairs + per_block - 1) / per_block));
-  cfg.blockDim = dim3(JOIN_THREADS);
-  cfg.stream = st;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return many ? cudaLaunchKernelEx(&cfg, paged_join_kernel<T, HD, 1>, s, a)
-              : cudaLaunchKernelEx(&cfg, paged_join_kernel<T, HD, 8>, s, a);
+  const unsigned blocks = (unsigned)((pairs + per_block - 1) / per_block);
+  return many ? launch_dependent(paged_join_kernel<T, HD, 1>, blocks, JOIN_THREADS, st, s, a)
+              : launch_dependent(paged_join_kernel<T, HD, 8>, blocks, JOIN_THREADS, st, s, a);
 }
 
 }  // namespace

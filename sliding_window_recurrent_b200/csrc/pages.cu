@@ -18,116 +18,164 @@ namespace {
 // page i of all pages handed out is S[|S| - 1 - i]. So one prefix sum over the
 // requests places every page, and then every token row is independent.
 //
-// The plan (one block: prefix sums over the requests) and the fill (a thread
-// per token row) are one launch when one block can do both, else two.
+// What bounds it is latency: a few KB are read and 16 bytes a token written. So the
+// plan (one block: prefix sums over the requests) takes one barrier a sum, the
+// fill (a thread per token row) finds its requests by block-wide counts instead of a
+// chain of probes, and is scheduled while the plan runs. Up to ONE_LAUNCH_ROWS rows
+// the plan's block does the rows itself.
 // ---------------------------------------------------------------------------
 struct PlanTotals {
   int64_t n_old, avail, left;  // free pages before, with the returned ones, after
+  int finished;                // requests
 };
 struct PlanViews {
   PlanTotals* totals;
-  int64_t* start;  // [B] first position of a served request's tokens, else -1
-  int* need_ex;    // [B] pages handed out to earlier requests
-  int* rel_ex;     // [B+1] pages returned by earlier requests
+  int2* req;  // [B] first position of a served request's tokens (else -1), pages handed out to earlier requests
+  int2* fin;  // [finished] pages returned up to and with a finished request, and which it is
 };
-__host__ __device__ inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-__host__ __device__ inline PlanViews plan_views(void* ws, int B) {
+__device__ __forceinline__ PlanViews plan_views(void* ws, int B) {
   char* p = static_cast<char*>(ws);
   PlanViews v;
   v.totals = reinterpret_cast<PlanTotals*>(p);
-  v.start = reinterpret_cast<int64_t*>(p + 256);
-  v.need_ex = reinterpret_cast<int*>(p + 256 + up256((size_t)B * 8));
-  v.rel_ex = v.need_ex + B;
+  v.req = reinterpret_cast<int2*>(p + 256);
+  v.fin = v.req + B;
   return v;
 }
 
-constexpr int PLAN_THREADS = 1024;
-constexpr int FILL_THREADS = 256;
-constexpr int FILL_ROWS = 1024;  // token rows of one block of the fill
+constexpr int PLAN_THREADS = 1024;  // at most
+constexpr int PLAN_EACH = 2;        // requests of a thread, kept in registers
+constexpr int FILL_ROWS = 256;      // token rows (and threads) of a block of the fill
 
-// Exclusive prefix sum over the block; *total receives the block's sum.
-template <typename T>
-__device__ __forceinline__ T block_exclusive(T x, T* sums /* [33] shared */, T* total) {
+// Exclusive prefix sums of x and y over the block, one barrier; sums of x stop at
+// `most` (saturating addition is associative). sums [32] is used once.
+__device__ __forceinline__ uint2 block_exclusive(uint2 v, uint32_t most, uint2* sums, uint2* total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  T inc = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  __syncthreads();  // the sums of an earlier call have been read
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  if (warp == 0) {
-    const T w = lane < PLAN_THREADS / 32 ? sums[lane] : T(0);
-    T winc = w;
+  auto scan = [&](uint2 z) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xffffffffu, winc, o);
-      if (lane >= o) winc += y;
+      const uint32_t x = __shfl_up_sync(0xffffffffu, z.x, o), y = __shfl_up_sync(0xffffffffu, z.y, o);
+      if (lane >= o) z = make_uint2(min(z.x + x, most), z.y + y);
     }
-    sums[lane] = winc - w;
-    if (lane == 31) sums[32] = winc;
-  }
+    return z;
+  };
+  auto from = [&](uint2 z, int l) {
+    return make_uint2(__shfl_sync(0xffffffffu, z.x, l), __shfl_sync(0xffffffffu, z.y, l));
+  };
+  const uint2 inc = scan(v);
+  if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  *total = sums[32];
-  return sums[warp] + inc - x;
+  // every warp sums the warps' sums for itself
+  const uint2 all = scan(lane < (int)blockDim.x / 32 ? sums[lane] : make_uint2(0, 0));
+  *total = from(all, 31);
+  const uint2 before = from(all, warp > 0 ? warp - 1 : 0), own = from(inc, lane > 0 ? lane - 1 : 0);
+  uint2 r = lane > 0 ? own : make_uint2(0, 0);
+  if (warp > 0) r = make_uint2(min(r.x + before.x, most), r.y + before.y);
+  return r;
 }
 
-// The first b in [lo, hi) with x[b] > t (hi if none): x is non-decreasing.
-template <typename T>
-__device__ __forceinline__ int first_above(const T* x, int lo, int hi, int64_t t) {
+// The first b in [lo, hi) with x(b) > t (hi if none): x is non-decreasing.
+template <typename X, typename V>
+__device__ __forceinline__ int first_above(X x, int lo, int hi, V t) {
   while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if ((int64_t)x[mid] > t) hi = mid;
+    const int mid = lo + (hi - lo) / 2;
+    if (x(mid) > t) hi = mid;
     else lo = mid + 1;
   }
   return lo;
 }
-
-// Page k of the pages that finished requests return (request, then column order).
-__device__ __forceinline__ int returned_page(const PageTablesArgs& a, const PlanViews& w, int64_t k) {
-  const int r = first_above(w.rel_ex + 1, 0, a.B, k);
-  if (r >= a.B) return -1;
-  return a.block_table[(int64_t)r * a.max_pages + (k - w.rel_ex[r])];
+// The same for two values t <= u and the whole block: each round reads a value a
+// thread and counts, so B requests take log(B) / log(threads) rounds of loads.
+__device__ __forceinline__ void block_first_above(const int64_t* x, int n, int64_t t, int64_t u, int* at, int* au) {
+  int lo[2] = {0, 0}, len[2] = {n, n};
+  while (len[0] > 0 || len[1] > 0) {
+    int64_t v[2];
+    int step[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // thread i stands for the `step` values from i * step
+      step[e] = (len[e] + (int)blockDim.x - 1) / (int)blockDim.x;
+      const int i = ((int)threadIdx.x + 1) * step[e] - 1;
+      v[e] = (int)threadIdx.x * step[e] < len[e] ? x[lo[e] + (i < len[e] ? i : len[e] - 1)] : INT64_MAX;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int before = __syncthreads_count(v[e] <= (e ? u : t)) * step[e];  // values in shares that lie before
+      lo[e] += before < len[e] ? before : len[e];
+      len[e] = step[e] > 1 && before < len[e] ? (len[e] - before < step[e] ? len[e] - before : step[e]) : 0;
+    }
+  }
+  *at = lo[0];
+  *au = lo[1];
 }
 
-// Token rows [t0, t0 + rows) of the map, and with them the table columns whose
+// Page k of the pages that finished requests return (request, then column order).
+__device__ __forceinline__ int returned_page(const PageTablesArgs& a, const int2* fin, int finished, int k) {
+  const int i = first_above([&](int j) { return fin[j].x; }, 0, finished, k);
+  if (i >= finished) return -1;
+  return a.block_table[(int64_t)fin[i].y * a.max_pages + (k - (i > 0 ? fin[i - 1].x : 0))];
+}
+
+// What a fill needs of the requests that its rows belong to.
+struct FillRequests {
+  int end[FILL_ROWS + 1];  // where their rows end, from the fill's first row; [0]: where the first request's begin
+  int2 at[FILL_ROWS];      // start, need_ex
+  int2 fin[FILL_ROWS];     // finished requests, if there are no more
+};
+// The finished requests, staged (a barrier has to follow before they are used).
+__device__ __forceinline__ const int2* stage_finished(const PlanViews& w, int finished, FillRequests& f) {
+  if (finished > FILL_ROWS) return w.fin;
+  for (int i = threadIdx.x; i < finished; i += blockDim.x) f.fin[i] = w.fin[i];
+  return f.fin;
+}
+
+// Token rows [t0, t0 + FILL_ROWS) of the map, and with them the table columns whose
 // page a row is the first of.
-__device__ void fill_rows(const PageTablesArgs& a, const PlanViews& w, int shift, int64_t t0, int rows, int* range,
-                          int* err) {
-  const int64_t t1 = t0 + rows < a.n_tokens ? t0 + rows : a.n_tokens;
-  const PlanTotals tot = *w.totals;
-  if (a.pad == 0) {  // the requests these rows belong to
-    if (threadIdx.x == 0) range[0] = first_above(a.cu_tokens + 1, 0, a.B, t0);
-    if (threadIdx.x == 32) range[1] = first_above(a.cu_tokens + 1, 0, a.B, t1 - 1);
-    __syncthreads();
+__device__ void fill_rows(const PageTablesArgs& a, const PlanViews& w, const PlanTotals& tot, const int2* fin, int shift,
+                          int64_t t0, FillRequests& f, int* err) {
+  const int64_t t1 = t0 + FILL_ROWS < a.n_tokens ? t0 + FILL_ROWS : a.n_tokens;
+  int b0 = 0, b1 = 0;  // the requests these rows belong to
+  if (a.pad == 0) block_first_above(a.cu_tokens + 1, a.B, t0, t1 - 1, &b0, &b1);
+  const bool staged = a.pad == 0 && b1 - b0 < FILL_ROWS;  // not with that many requests without rows between
+  if (staged) {
+    for (int i = threadIdx.x; i <= b1 - b0 + 1 && b0 + i <= a.B; i += blockDim.x) {
+      f.end[i] = (int)(a.cu_tokens[b0 + i] - t0);
+      if (i <= b1 - b0 && b0 + i < a.B) f.at[i] = w.req[b0 + i];
+    }
   }
+  __syncthreads();
   for (int64_t t = t0 + threadIdx.x; t < t1; t += blockDim.x) {
     int b;
-    int64_t i;
-    bool live;
-    if (a.pad == 0) {
-      b = first_above(a.cu_tokens + 1, range[0], range[1], t);
-      live = b < a.B && t < a.cu_tokens[a.B];
-      i = live ? t - a.cu_tokens[b] : 0;
-    } else {
+    int2 at = make_int2(-1, 0);
+    int64_t i = 0;
+    if (staged) {
+      const int x = (int)(t - t0), k = first_above([&](int j) { return f.end[j + 1]; }, 0, b1 - b0, x);
+      b = b0 + k;
+      if (b < a.B) {
+        i = x - f.end[k];
+        at = f.at[k];
+      }
+    } else if (a.pad > 0) {
       b = (int)(t / a.pad);
-      i = t - (int64_t)b * a.pad;
-      live = i < a.new_len[b];
+      i = t - b * a.pad;
+      if (i < a.new_len[b]) at = w.req[b];
+    } else {
+      b = first_above([&](int j) { return a.cu_tokens[j + 1]; }, b0, b1, t);
+      if (b < a.B) {
+        i = t - a.cu_tokens[b];
+        at = w.req[b];
+      }
     }
-    const int64_t start = live ? w.start[b] : -1;
+    const int start = at.x, need_ex = at.y;
     int64_t p = -1, slot = -1;
     if (start >= 0) {
       p = start + i;
-      const int64_t col = p >> shift, held = (start + a.page_size - 1) >> shift;
+      const int col = (int)(p >> shift), held = (start + a.page_size - 1) >> shift;
       int32_t* row = a.block_table + (int64_t)b * a.max_pages;
       int page;
       if (col < held) {
         page = row[col];  // the last page the request held already
       } else {
-        const int64_t s = tot.avail - 1 - (w.need_ex[b] + (col - held));
-        page = s < tot.n_old ? a.free_pages[s] : returned_page(a, w, s - tot.n_old);
+        const int64_t s = tot.avail - 1 - (need_ex + (col - held));
+        page = s < tot.n_old ? a.free_pages[s] : returned_page(a, fin, tot.finished, (int)(s - tot.n_old));
         if ((p & (a.page_size - 1)) == 0) row[col] = page;  // the page's first token names it in the table
       }
       if (page >= 0 && page < a.num_pages) {
@@ -143,91 +191,133 @@ __device__ void fill_rows(const PageTablesArgs& a, const PlanViews& w, int shift
 }
 
 // Returned pages that no request took stay on the stack: entries n_old..left-1.
-__device__ void push_returned(const PageTablesArgs& a, const PlanViews& w, int64_t first, int64_t step, int* err) {
-  const PlanTotals tot = *w.totals;
+__device__ void push_returned(const PageTablesArgs& a, const PlanTotals& tot, const int2* fin, int64_t first, int64_t step,
+                              int* err) {
   for (int64_t j = tot.n_old + first; j < tot.left; j += step) {
     if (j >= a.num_pages) {  // more pages returned than the pool has
       record_error(err, DEV_BOUNDS);
       break;
     }
-    a.free_pages[j] = returned_page(a, w, j - tot.n_old);
+    a.free_pages[j] = returned_page(a, fin, tot.finished, (int)(j - tot.n_old));
   }
 }
 
-// One block. The prefix sums run over chunks of 1024 requests, so B is not
-// bounded by the block; with `fill` it also does the (few) token rows.
+// One block. It takes the requests in chunks of PLAN_EACH per thread (one chunk, where
+// there are no more). With `fill` it also does the (few) token rows.
 __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs a, void* ws, int shift, int fill,
                                                                  int* err) {
-  __shared__ int64_t sums64[33];
-  __shared__ int sums32[33];
-  __shared__ int range[2];
+  __shared__ uint2 sums[4][32];
+  __shared__ FillRequests requests;
+  asm volatile("griddepcontrol.launch_dependents;");
   const PlanViews w = plan_views(ws, a.B);
-  const int tid = threadIdx.x;
-  const int64_t cap = (int64_t)a.max_pages << shift;
-  auto held_of = [&](int64_t c) -> int {  // pages of c cached tokens; lengths outside the row are cut
-    c = c < 0 ? 0 : (c > cap ? cap : c);
-    return (int)((c + a.page_size - 1) >> shift);
-  };
-  int mine = 0, released;
-  for (int b = tid; b < a.B; b += PLAN_THREADS)
-    if (a.new_len[b] < 0) mine += held_of(a.ctx_len[b]);
-  block_exclusive(mine, sums32, &released);
-  int64_t n_old = *a.n_free;
-  if (n_old < 0 || n_old > a.num_pages) {
-    if (tid == 0) record_error(err, DEV_BOUNDS);
-    n_old = n_old < 0 ? 0 : a.num_pages;
+  const int tid = threadIdx.x, chunk = PLAN_EACH * blockDim.x;
+  const int cap = a.max_pages << shift;  // at most 2^30, like n_tokens
+  const uint32_t most = (uint32_t)a.n_tokens + 1;
+  auto pages_of = [&](int len) { return (len + a.page_size - 1) >> shift; };
+  // a length outside its row is cut for what it holds, and never served (cap + 1)
+  auto clip = [&](int64_t c) { return c < 0 || c > cap ? cap + 1 : (int)c; };
+  auto held_of = [&](int64_t c) { return pages_of(c < 0 ? 0 : (c > cap ? cap : (int)c)); };
+  int n_old = *a.n_free, released = 0;
+  if (a.B > chunk) {  // pages come back before any is handed out
+    uint2 total;
+    uint32_t rel = 0;
+    for (int b = tid; b < a.B; b += blockDim.x)
+      if (a.new_len[b] < 0) rel += held_of(a.ctx_len[b]);
+    block_exclusive(make_uint2(0, rel), most, sums[3], &total);
+    released = total.y;
   }
-  const int64_t avail = n_old + released;
-  int64_t rows_before = 0, need_before = 0;
-  int rel_before = 0, taken = 0;
-  for (int base = 0; base < a.B; base += PLAN_THREADS) {
-    const int b = base + tid;
-    const bool in = b < a.B;
-    const int64_t c = in ? a.ctx_len[b] : 0, n = in ? a.new_len[b] : 0;
-    const bool done = n < 0;
-    // one row more than there are is as bad as any number of them, and keeps the sum small
-    const int64_t rows = n < 0 ? 0 : (n > a.n_tokens ? a.n_tokens + 1 : n);
-    const int held = held_of(c);
-    int64_t chunk_rows, chunk_need;
-    int chunk_rel;
-    const int64_t row_end = rows_before + block_exclusive(rows, sums64, &chunk_rows) + rows;
-    const int rel_ex = rel_before + block_exclusive(done ? held : 0, sums32, &chunk_rel);
-    const bool fits = in && !done && c >= 0 && c <= cap - rows && (a.pad ? rows <= a.pad : row_end <= a.n_tokens);
-    const int need = fits ? held_of(c + rows) - held : 0;
-    const int64_t need_ex = need_before + block_exclusive((int64_t)need, sums64, &chunk_need);
-    const bool served = fits && (need == 0 || need_ex + need <= avail);
-    if (in) {
-      if (b == 0) a.cu_tokens[0] = 0;
-      a.cu_tokens[b + 1] = row_end < a.n_tokens ? row_end : a.n_tokens;
-      a.seq_len[b] = done ? 0 : (served ? c + rows : c);
-      w.start[b] = served ? c : -1;
-      w.need_ex[b] = served ? (int)need_ex : 0;
-      if (b == 0) w.rel_ex[0] = 0;
-      w.rel_ex[b + 1] = rel_ex + (done ? held : 0);
+  uint2 before = make_uint2(0, 0);  // rows and returned pages of earlier chunks
+  uint32_t need_before = 0, fin_before = 0, taken = 0;
+  for (int base = 0; base < a.B; base += chunk) {
+    const int b0 = base + tid * PLAN_EACH;
+    int c[PLAN_EACH], held[PLAN_EACH];
+    uint32_t rows[PLAN_EACH];  // one row more than there are is as bad as any number of them
+    bool done[PLAN_EACH];
+    int64_t ctx[PLAN_EACH];
+    uint2 v = make_uint2(0, 0), total;
+#pragma unroll
+    for (int e = 0; e < PLAN_EACH; ++e) {
+      const bool in = b0 + e < a.B;
+      const int64_t n = in ? a.new_len[b0 + e] : 0;
+      ctx[e] = in ? a.ctx_len[b0 + e] : 0;
+      c[e] = clip(ctx[e]);
+      held[e] = held_of(ctx[e]);
+      done[e] = n < 0;
+      rows[e] = n < 0 ? 0 : (n > a.n_tokens ? most : (uint32_t)n);
+      v.x = min(v.x + rows[e], most);
+      v.y += done[e] ? held[e] : 0;
     }
-    if (served) taken += need;
-    rows_before += chunk_rows;
-    need_before += chunk_need;
-    rel_before += chunk_rel;
+    if (base > 0) __syncthreads();  // the sums of the last chunk have been read
+    uint2 at = block_exclusive(v, most, sums[0], &total);
+    at = make_uint2(min(at.x + before.x, most), at.y + before.y);
+    before = make_uint2(min(before.x + total.x, most), before.y + total.y);
+    uint32_t end[PLAN_EACH], need[PLAN_EACH], mine = 0, ends = 0;
+    bool fits[PLAN_EACH];
+#pragma unroll
+    for (int e = 0; e < PLAN_EACH; ++e) {
+      at.x = min(at.x + rows[e], most);
+      end[e] = at.x;
+      fits[e] = b0 + e < a.B && !done[e] && c[e] <= cap && rows[e] <= (uint32_t)(cap - c[e]) &&
+                (a.pad ? rows[e] <= a.pad : end[e] < most);
+      need[e] = fits[e] ? pages_of(c[e] + (int)rows[e]) - held[e] : 0;
+      mine += need[e];
+      ends += done[e];
+    }
+    const uint2 pre = block_exclusive(make_uint2(ends, mine), ~0u, sums[1], &total);
+    uint32_t need_ex = need_before + pre.y, fin_ex = fin_before + pre.x;
+    need_before += total.y;
+    fin_before += total.x;
+    if (a.B <= chunk) released = before.y;
+    if (base == 0) {
+      if (n_old < 0 || n_old > a.num_pages) {
+        if (tid == 0) record_error(err, DEV_BOUNDS);
+        n_old = n_old < 0 ? 0 : a.num_pages;
+      }
+      if (tid == 0) a.cu_tokens[0] = 0;
+    }
+#pragma unroll
+    for (int e = 0; e < PLAN_EACH; ++e) {
+      const int b = b0 + e;
+      if (b >= a.B) break;
+      const bool served = fits[e] && (need[e] == 0 || (int64_t)need_ex + need[e] <= (int64_t)n_old + released);
+      if (done[e]) {
+        at.y += held[e];
+        w.fin[fin_ex++] = make_int2((int)at.y, b);
+      }
+      a.cu_tokens[b + 1] = end[e] < most ? end[e] : a.n_tokens;
+      a.seq_len[b] = done[e] ? 0 : (served ? ctx[e] + rows[e] : ctx[e]);
+      w.req[b] = make_int2(served ? c[e] : -1, (int)need_ex);
+      need_ex += need[e];
+      taken += served ? need[e] : 0;
+    }
   }
-  int all_taken;
-  block_exclusive(taken, sums32, &all_taken);
+  uint2 total;
+  block_exclusive(make_uint2(0, taken), most, sums[2], &total);
+  const int64_t avail = (int64_t)n_old + released;
+  const PlanTotals tot{n_old, avail, avail - (int)total.y, (int)fin_before};
   if (tid == 0) {
-    const int64_t left = avail - all_taken;
-    *w.totals = PlanTotals{n_old, avail, left};
-    *a.n_free_out = (int)(left < a.num_pages ? left : a.num_pages);
+    *w.totals = tot;
+    *a.n_free_out = (int)(tot.left < a.num_pages ? tot.left : a.num_pages);
   }
   if (!fill) return;
   __syncthreads();  // the plan is visible to the block
-  if (a.n_tokens > 0) fill_rows(a, w, shift, 0, (int)a.n_tokens, range, err);
-  push_returned(a, w, tid, PLAN_THREADS, err);
+  const int2* fin = stage_finished(w, tot.finished, requests);
+  __syncthreads();
+  for (int64_t t0 = 0; t0 < a.n_tokens; t0 += FILL_ROWS) {
+    if (t0 > 0) __syncthreads();  // the requests of the last rows have been read
+    fill_rows(a, w, tot, fin, shift, t0, requests, err);
+  }
+  push_returned(a, tot, fin, tid, blockDim.x, err);
 }
 
-__global__ void __launch_bounds__(FILL_THREADS) page_fill_kernel(PageTablesArgs a, void* ws, int shift, int* err) {
-  __shared__ int range[2];
+__global__ void __launch_bounds__(FILL_ROWS) page_fill_kernel(PageTablesArgs a, void* ws, int shift, int* err) {
+  __shared__ FillRequests requests;
   const PlanViews w = plan_views(ws, a.B);
-  fill_rows(a, w, shift, (int64_t)blockIdx.x * FILL_ROWS, FILL_ROWS, range, err);
-  push_returned(a, w, (int64_t)blockIdx.x * FILL_THREADS + threadIdx.x, (int64_t)gridDim.x * FILL_THREADS, err);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+  const PlanTotals tot = *w.totals;
+  const int2* fin = stage_finished(w, tot.finished, requests);
+  fill_rows(a, w, tot, fin, shift, (int64_t)blockIdx.x * FILL_ROWS, requests, err);  // has a barrier before it reads fin
+  push_returned(a, tot, fin, (int64_t)blockIdx.x * FILL_ROWS + threadIdx.x, (int64_t)gridDim.x * FILL_ROWS, err);
 }
 
 // ---------------------------------------------------------------------------
@@ -345,24 +435,26 @@ cudaError_t write_pages(const PagedShape& s, int64_t n, const int64_t* slots, co
   return cudaGetLastError();
 }
 
-// Token rows that one block of the plan fills itself instead of a second launch.
-constexpr int64_t ONE_LAUNCH_ROWS = 4096;
+// Token rows that the plan's block fills itself.
+constexpr int64_t ONE_LAUNCH_ROWS = 1024;
 
 }  // namespace
 
-size_t page_tables_workspace_bytes(int B) { return 256 + up256((size_t)B * 8) + up256(((size_t)2 * B + 1) * 4); }
+size_t page_tables_workspace_bytes(int B) { return 256 + (size_t)B * 2 * sizeof(int2); }
 
 int page_tables_kernels(int64_t n_tokens) { return n_tokens <= ONE_LAUNCH_ROWS ? 1 : 2; }
 
 cudaError_t launch_page_tables(const PageTablesArgs& a, void* workspace, int* err, cudaStream_t st) {
   const int shift = log2_of(a.page_size);
   const int one = a.n_tokens <= ONE_LAUNCH_ROWS;
-  page_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a, workspace, shift, one, err);
+  int threads = (a.B + PLAN_EACH - 1) / PLAN_EACH;  // few requests: fewer warps to sum over
+  if (one && a.n_tokens > threads) threads = (int)a.n_tokens;
+  threads = threads < 64 ? 64 : threads > PLAN_THREADS ? PLAN_THREADS : (threads + 31) / 32 * 32;
+  page_plan_kernel<<<1, threads, 0, st>>>(a, workspace, shift, one, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || one) return e;
-  page_fill_kernel<<<(unsigned)((a.n_tokens + FILL_ROWS - 1) / FILL_ROWS), FILL_THREADS, 0, st>>>(a, workspace, shift,
-                                                                                                  err);
-  return cudaGetLastError();
+  return launch_dependent(page_fill_kernel, (unsigned)((a.n_tokens + FILL_ROWS - 1) / FILL_ROWS), FILL_ROWS, st, a,
+                          workspace, shift, err);
 }
 
 cudaError_t launch_paged_write(const PagedShape& s, int64_t n, const int64_t* slots, const int64_t* pos, const void* k,
