@@ -322,97 +322,142 @@ __global__ void __launch_bounds__(FILL_ROWS) page_fill_kernel(PageTablesArgs a, 
 
 // ---------------------------------------------------------------------------
 // Entries into pages. A thread owns 8 RoPE pairs of one (token, head) row:
-// channels [8u, 8u+8) and [hd/2 + 8u, hd/2 + 8u + 8), loaded and stored 16
-// bytes at a time; hd/16 threads cover a row and reduce its RMS with shuffles.
-// A block takes `tile` tokens; their angles (double products, shared by the
-// heads) are formed once into shared memory.
+// channels [8u, 8u+8) and [hd/2 + 8u, hd/2 + 8u + 8), loaded and stored 16 bytes
+// at a time; hd/16 threads cover a row and reduce its RMS with shuffles. A thread
+// keeps its head (and gates) and goes through the block's tokens, `pass` of them
+// at a time; their angles (double products, shared by the heads) are formed once
+// into shared memory while the first loads are on their way.
 // ---------------------------------------------------------------------------
 enum { WRITE_COPY = 0, WRITE_ROPE = 1, WRITE_MIX = 2 };
 constexpr int WRITE_THREADS = 256;
-constexpr int WRITE_TILE = 16;  // the most tokens of a block
+constexpr int WRITE_TURNS = 2048;  // angles of a block: 32 tokens of hd 128, 64 of hd 64
+
+// 8 elements as they are stored, so that all loads are in flight before any arithmetic.
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void store_raw8(T* p, const Raw8<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
+}
 
 template <typename T, int HD, int MODE>
-__global__ void __launch_bounds__(WRITE_THREADS) paged_write_kernel(
-    PagedShape s, RopeFreqs rf, int shift, int64_t n, int tile, const int64_t* __restrict__ slots,
-    const int64_t* __restrict__ pos, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ Rk,
-    const T* __restrict__ Rv, const float* __restrict__ gates, T* __restrict__ kp, T* __restrict__ vp, int* err) {
+__global__ void __launch_bounds__(WRITE_THREADS, sizeof(T) == 2 ? 3 : 2) paged_write_kernel(
+    PagedShape s, const __grid_constant__ RopeFreqs rf, int shift, int64_t n, int tile, int heads, int pass,
+    const int64_t* __restrict__ slots, const int64_t* __restrict__ pos, const T* __restrict__ k,
+    const T* __restrict__ v, const T* __restrict__ Rk, const T* __restrict__ Rv, const float* __restrict__ gates,
+    T* __restrict__ kp, T* __restrict__ vp, int* err) {
   constexpr int HALF = HD / 2, TPR = HD / 16;
-  __shared__ float2 turn[MODE == WRITE_COPY ? 1 : WRITE_TILE * HALF];
+  __shared__ float2 turn[MODE == WRITE_COPY ? 1 : WRITE_TURNS];
   const int64_t t0 = (int64_t)blockIdx.x * tile;
   const int ntok = (int)(n - t0 < tile ? n - t0 : tile);
+  const int64_t nslots = (int64_t)s.num_pages << shift;
+  const int u = threadIdx.x % TPR, row = threadIdx.x / TPR, h = blockIdx.y * heads + row % heads;
+  const bool mine = row < heads * pass && h < s.Hkv;
+  float gkl = 1.f, gkr = 0.f, gvl = 1.f, gvr = 0.f;
+  Raw8<T> k1{}, k2{}, v1{}, v2{}, r1{}, r2{}, w1{}, w2{};
+  int64_t slot = -1;
+  auto load = [&](int tt) {  // every load of token tt's piece; slot < 0: nothing to write
+    slot = -1;
+    if (!mine || tt >= ntok) return;
+    slot = slots[t0 + tt];
+    if (MODE != WRITE_COPY && pos[t0 + tt] < 0) slot = -1;
+    if (slot >= nslots) {
+      if (u == 0) record_error(err, DEV_BOUNDS);
+      slot = -1;
+    }
+    const int64_t src = ((t0 + tt) * s.Hkv + h) * HD + 8 * u;
+    k1 = raw8(k + src);
+    k2 = raw8(k + src + HALF);
+    v1 = raw8(v + src);
+    v2 = raw8(v + src + HALF);
+    if (MODE == WRITE_MIX) {
+      r1 = raw8(Rk + src);
+      r2 = raw8(Rk + src + HALF);
+      w1 = raw8(Rv + src);
+      w2 = raw8(Rv + src + HALF);
+    }
+  };
+  load(row / heads);
+  if (MODE == WRITE_MIX && mine) {
+    gkl = gate_value(gates[h]);
+    gkr = gate_value(gates[s.Hkv + h]);
+    gvl = gate_value(gates[s.vg * s.Hkv + h]);
+    gvr = gate_value(gates[(s.vg + 1) * s.Hkv + h]);
+  }
   if (MODE != WRITE_COPY) {
     for (int i = threadIdx.x; i < ntok * HALF; i += WRITE_THREADS)
       turn[i] = rope_turn(pos[t0 + i / HALF], rf.turns[i % HALF]);
     __syncthreads();
   }
-  const int64_t nslots = (int64_t)s.num_pages << shift;
-  const int items = ntok * s.Hkv * TPR;
-  for (int i0 = 0; i0 < items; i0 += WRITE_THREADS) {  // whole warps: the RMS sums shuffle
-    const int i = i0 + threadIdx.x;
-    const int u = i % TPR, row = i / TPR;
-    bool live = i < items;
-    const int tt = live ? row / s.Hkv : 0, h = live ? row % s.Hkv : 0;
-    const int64_t slot = slots[t0 + tt];
-    if (live && slot >= nslots) {
-      if (u == 0) record_error(err, DEV_BOUNDS);
-      live = false;
-    }
-    live = live && slot >= 0 && (MODE == WRITE_COPY || pos[t0 + tt] >= 0);
-    const int64_t src = ((t0 + tt) * s.Hkv + h) * HD + 8 * u;
-    float k1[8], k2[8], v1[8], v2[8], r1[8], r2[8];
-    float ss = 0.f;
-    if (live) {
-      load8f(k + src, k1);
-      load8f(k + src + HALF, k2);
-      load8f(v + src, v1);
-      load8f(v + src + HALF, v2);
-      if (MODE == WRITE_MIX) {
-        load8f(Rk + src, r1);
-        load8f(Rk + src + HALF, r2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss += r1[e] * r1[e] + r2[e] * r2[e];
-      }
-    }
+  for (int tt = row / heads; tt - row / heads < ntok; tt += pass) {  // whole blocks: the RMS sums shuffle
+    float x1[8], x2[8], y1[8], y2[8];
+    float rinv = 0.f;
     if (MODE == WRITE_MIX) {
+      load8f(reinterpret_cast<const T*>(&r1), y1);
+      load8f(reinterpret_cast<const T*>(&r2), y2);
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += y1[e] * y1[e] + y2[e] * y2[e];
 #pragma unroll
       for (int o = TPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      rinv = gkr * rsqrtf(ss / HD + s.eps);
     }
-    if (!live) continue;
-    if (MODE != WRITE_COPY) {
-      const float rinv = MODE == WRITE_MIX ? rsqrtf(ss / HD + s.eps) : 0.f;
-      float gkl = 1.f, gkr = 0.f;
-      if (MODE == WRITE_MIX) {
-        gkl = gate_value(gates[h]);
-        gkr = gate_value(gates[s.Hkv + h]);
-      }
+    if (slot >= 0) {
+      const int64_t dst = ((((slot >> shift) * s.Hkv + h) << shift) + (slot & (s.page_size - 1))) * HD + 8 * u;
+      if (MODE == WRITE_COPY) {
+        store_raw8(kp + dst, k1);
+        store_raw8(kp + dst + HALF, k2);
+      } else {
+        load8f(reinterpret_cast<const T*>(&k1), x1);
+        load8f(reinterpret_cast<const T*>(&k2), x2);
+        const float4* tw = reinterpret_cast<const float4*>(turn + tt * HALF + 8 * u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 w = turn[tt * HALF + 8 * u + e];
-        float a = k1[e] * w.x - k2[e] * w.y, b = k1[e] * w.y + k2[e] * w.x;
-        if (MODE == WRITE_MIX) {
-          const float x = r1[e] * rinv, y = r2[e] * rinv;
-          a = gkl * a + gkr * (x * w.x - y * w.y);
-          b = gkl * b + gkr * (x * w.y + y * w.x);
+        for (int e = 0; e < 8; e += 2) {
+          const float4 w = tw[e / 2];  // two pairs' angles
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float cs = i ? w.z : w.x, sn = i ? w.w : w.y;
+            // both keys turn by the same angle, so the mix comes first
+            float p = x1[e + i], q = x2[e + i];
+            if (MODE == WRITE_MIX) {
+              p = gkl * p + rinv * y1[e + i];
+              q = gkl * q + rinv * y2[e + i];
+            }
+            x1[e + i] = p * cs - q * sn;
+            x2[e + i] = p * sn + q * cs;
+          }
         }
-        k1[e] = a;
-        k2[e] = b;
+        store8f(kp + dst, x1);
+        store8f(kp + dst + HALF, x2);
       }
-    }
-    if (MODE == WRITE_MIX) {
-      const float gvl = gate_value(gates[s.vg * s.Hkv + h]), gvr = gate_value(gates[(s.vg + 1) * s.Hkv + h]);
-      load8f(Rv + src, r1);
-      load8f(Rv + src + HALF, r2);
+      if (MODE != WRITE_MIX) {
+        store_raw8(vp + dst, v1);
+        store_raw8(vp + dst + HALF, v2);
+      } else {
+        load8f(reinterpret_cast<const T*>(&v1), x1);
+        load8f(reinterpret_cast<const T*>(&v2), x2);
+        load8f(reinterpret_cast<const T*>(&w1), y1);
+        load8f(reinterpret_cast<const T*>(&w2), y2);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v1[e] = gvl * v1[e] + gvr * r1[e];
-        v2[e] = gvl * v2[e] + gvr * r2[e];
+        for (int e = 0; e < 8; ++e) {
+          x1[e] = gvl * x1[e] + gvr * y1[e];
+          x2[e] = gvl * x2[e] + gvr * y2[e];
+        }
+        store8f(vp + dst, x1);
+        store8f(vp + dst + HALF, x2);
       }
     }
-    const int64_t dst = ((((slot >> shift) * s.Hkv + h) << shift) + (slot & (s.page_size - 1))) * HD + 8 * u;
-    store8f(kp + dst, k1);
-    store8f(kp + dst + HALF, k2);
-    store8f(vp + dst, v1);
-    store8f(vp + dst + HALF, v2);
+    load(tt + pass);
   }
 }
 
@@ -420,14 +465,18 @@ template <typename T, int HD>
 cudaError_t write_pages(const PagedShape& s, int64_t n, const int64_t* slots, const int64_t* pos, const void* k,
                         const void* v, const void* Rk, const void* Rv, const float* gates, void* kp, void* vp, int* err,
                         cudaStream_t st) {
-  int tile = WRITE_TILE;
-  while (tile > 1 && n < (int64_t)tile * 2 * num_sms()) tile /= 2;  // few tokens: spread them over the SMs
-  const unsigned blocks = (unsigned)((n + tile - 1) / tile);
-  const RopeFreqs rf = rope_freqs(HD, s.log2_base);
+  constexpr int ROWS = WRITE_THREADS / (HD / 16), MOST = WRITE_TURNS / (HD / 2);
+  const int heads = s.Hkv < ROWS ? s.Hkv : ROWS, pass = ROWS / heads;  // of a block; tokens at a time
+  // two passes a block: one leaves the angles uncovered, four leave a ragged last wave
+  // (8192 mixed rows of 10 x 128 bf16: 27.3, 26.2, 27.8 us with 1, 2, 4 passes)
+  int tile = pass * 2 < MOST ? pass * 2 : MOST;
+  while (tile > 1 && n < (int64_t)tile * 4 * num_sms()) tile /= 2;  // few tokens: spread them over the SMs
+  const dim3 blocks((unsigned)((n + tile - 1) / tile), (unsigned)((s.Hkv + heads - 1) / heads));
+  const RopeFreqs& rf = rope_freqs(HD, s.log2_base);
   const int shift = log2_of(s.page_size);
   auto go = [&](auto kern) {
-    kern<<<blocks, WRITE_THREADS, 0, st>>>(s, rf, shift, n, tile, slots, pos, (const T*)k, (const T*)v, (const T*)Rk,
-                                           (const T*)Rv, gates, (T*)kp, (T*)vp, err);
+    kern<<<blocks, WRITE_THREADS, 0, st>>>(s, rf, shift, n, tile, heads, pass, slots, pos, (const T*)k, (const T*)v,
+                                           (const T*)Rk, (const T*)Rv, gates, (T*)kp, (T*)vp, err);
   };
   if (!pos) go(paged_write_kernel<T, HD, WRITE_COPY>);
   else if (!s.inject) go(paged_write_kernel<T, HD, WRITE_ROPE>);
