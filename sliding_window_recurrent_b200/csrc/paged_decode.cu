@@ -444,6 +444,7 @@ struct DecodeArgs {
   void *kp, *vp, *out;
   float* parts;      // [warps][2][heads][PART_ROW]
   int warps;         // of the grid
+  double inv_warps;
   int shift;         // log2 of the page size
   int heads, units;  // query heads of a unit (the last may have fewer), units of a sequence
   float scale_log2;
@@ -472,40 +473,53 @@ __device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeAr
 // kernels forms the same sums. Thread i covers `chunk` sequences from i * chunk.
 template <int THREADS>
 struct Plan {
-  int64_t before[THREADS + 1];  // steps (of one unit each) of the sequences before thread i's
+  int64_t before[THREADS];  // steps (of one unit each) of the sequences before thread i's
   int64_t sums[THREADS / 32];
-  int chunk;
-
-  __device__ __forceinline__ void form(const PagedShape& s, const DecodeArgs& a) {  // ends in a barrier
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int per = (s.B + THREADS - 1) / THREADS;
-    int64_t mine = 0;
-    for (int b = tid * per; b < (tid + 1) * per && b < s.B; ++b) mine += sequence(s, a, b).n;
-    int64_t inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    int64_t base = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w)
-      if (w < warp) base += sums[w];
-    before[tid + 1] = base + inc;
-    if (tid == 0) {
-      before[0] = 0;
-      chunk = per;
-    }
-    __syncthreads();
-  }
-  // steps of a warp's range
-  __device__ __forceinline__ int64_t range(const DecodeArgs& a) const {
-    const int64_t per = (before[THREADS] * a.units + a.warps - 1) / a.warps;
-    return per < MIN_STEPS ? MIN_STEPS : per;
-  }
+  int owner[THREADS / 32];  // the thread whose sequences hold the first step of the block's warp w
 };
+// What a thread keeps of it.
+struct Steps {
+  int64_t total, per;  // steps of all units, of a warp's range
+  int chunk;
+};
+template <int THREADS>
+__device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape& s, const DecodeArgs& a) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  Steps r;
+  r.chunk = (s.B + THREADS - 1) / THREADS;
+  int64_t mine = 0;
+  for (int b = tid * r.chunk; b < (tid + 1) * r.chunk && b < s.B; ++b) mine += sequence(s, a, b).n;
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) plan.sums[warp] = inc;
+  __syncthreads();
+  int64_t at = inc - mine;
+  r.total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) at += plan.sums[w];
+    r.total += plan.sums[w];
+  }
+  plan.before[tid] = at;
+  r.total *= a.units;
+  // total / warps, rounded up (a 64-bit division would take 0.3 us here)
+  r.per = r.total > 0 ? (int64_t)((double)(r.total - 1) * a.inv_warps) + 1 : 1;
+  if (r.per * a.warps < r.total) ++r.per;
+  if (r.per < MIN_STEPS) r.per = MIN_STEPS;
+  at *= a.units;
+  mine *= a.units;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int64_t t = r.per * ((int64_t)blockIdx.x * (THREADS / 32) + w) - at;
+    if (t >= 0 && t < mine) plan.owner[w] = tid;
+  }
+  __syncthreads();
+  return r;
+}
 
 // The unit that a global step lies in: sequence, unit within it, its first step.
 struct Cursor {
@@ -513,23 +527,22 @@ struct Cursor {
   Sequence q;
   int64_t base;
 };
+// The one of step t, which thread `owner`'s sequences hold.
 template <int THREADS>
-__device__ __forceinline__ Cursor locate(const Plan<THREADS>& plan, const PagedShape& s, const DecodeArgs& a, int64_t t) {
-  int lo = 0, hi = THREADS - 1;  // the first chunk whose steps end after t
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (plan.before[mid + 1] * a.units > t) hi = mid;
-    else lo = mid + 1;
-  }
+__device__ __forceinline__ Cursor locate(const Plan<THREADS>& plan, const Steps& steps, const PagedShape& s,
+                                         const DecodeArgs& a, int owner, int64_t t) {
   Cursor c;
-  c.b = lo * plan.chunk;
-  int64_t at = plan.before[lo] * a.units;
+  c.b = owner * steps.chunk;
+  int64_t at = plan.before[owner] * a.units;
   for (;; ++c.b) {
     c.q = sequence(s, a, c.b);
     if (t < at + (int64_t)c.q.n * a.units) break;
     at += (int64_t)c.q.n * a.units;
   }
-  c.hu = (int)((t - at) / c.q.n);
+  const int64_t rest = t - at;
+  c.hu = (int)((float)rest / (float)c.q.n);  // off by one at most: units are few
+  if ((int64_t)c.hu * c.q.n > rest) --c.hu;
+  if ((int64_t)(c.hu + 1) * c.q.n <= rest) ++c.hu;
   c.base = at + (int64_t)c.hu * c.q.n;
   return c;
 }
@@ -564,13 +577,13 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
   T* out = static_cast<T*>(a.out);
 
   asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks may take the places that come free
-  plan.form(s, a);
-  const int64_t per = plan.range(a), total = plan.before[NW * 32] * a.units;
+  const Steps steps = form_plan(plan, s, a);
+  const int64_t per = steps.per, total = steps.total;
   const int me = blockIdx.x * NW + warp;
   const int64_t t0 = per * me, t1 = t0 + per < total ? t0 + per : total;  // the warp's range
   if (t0 >= t1) return;
   const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;  // units, query heads of a key/value head
-  Cursor cur = locate(plan, s, a, t0);  // the unit being worked on
+  Cursor cur = locate(plan, steps, s, a, plan.owner[warp], t0);  // the unit being worked on
 
   // ---- copies
   Cursor ahead = cur;
@@ -756,18 +769,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedShape s, 
   __shared__ float4 so[NW][V];
   __shared__ float sm[NW], sl[NW];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  plan.form(s, a);  // reads nothing that the first kernel writes
+  const Steps steps = form_plan(plan, s, a);  // reads nothing that the first kernel writes
   const int64_t pair = (int64_t)blockIdx.x * (NW / JW) + warp / JW;
   const bool in = pair < (int64_t)s.B * s.H;
   const int b = in ? (int)(pair / s.H) : 0, h = in ? (int)(pair % s.H) : 0;
   const Sequence q = sequence(s, a, b);
   const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
   const int hk = h / per_kv, in_kv = h - hk * per_kv, j = in_kv % a.heads;
-  const int i = b / plan.chunk;
+  const int i = b / steps.chunk;
   int64_t base = plan.before[i];
-  for (int x = i * plan.chunk; x < b; ++x) base += sequence(s, a, x).n;
+  for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).n;
   base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.n;  // the unit's first step
-  const int64_t per = plan.range(a);
+  const int64_t per = steps.per;
   const int w0 = (int)(base / per), np = q.n ? (int)((base + q.n - 1) / per) - w0 + 1 : 0;  // warps with a part
   const int64_t stride = (int64_t)2 * a.heads * PART_ROW;
   // warp w0's part may follow other units in its range; the others begin with this unit
@@ -879,6 +892,7 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   int64_t grid = (int64_t)num_sms() * OCC;
   if (grid > most) grid = most;
   a.warps = (int)grid * NW;
+  a.inv_warps = 1.0 / a.warps;
   kern<<<(unsigned)grid, NW * 32, smem, st>>>(s, a, rope_freqs(HD, s.log2_base));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
