@@ -193,9 +193,19 @@ struct MmaTile {
       for (int e = 0; e < 4; ++e) {
         s[n][e] += s2[n][e];
         if (ONE) s[n][e] += __shfl_xor_sync(0xffffffffu, s[n][e], 2);
-        if (!all && !live(g + (e & 2) * 4)) s[n][e] = -INFINITY;
-        grow |= s[n][e] > m[n][e & 1] + SLACK;
       }
+    if (!all) {  // a branch of its own: most steps are whole
+      const bool on[2] = {live(g), live(g + 8)};
+#pragma unroll
+      for (int n = 0; n < NH; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!on[e / 2]) s[n][e] = -INFINITY;
+    }
+#pragma unroll
+    for (int n = 0; n < NH; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) grow |= s[n][e] > m[n][e & 1] + SLACK;
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int n = 0; n < NH; ++n)
@@ -587,46 +597,63 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
 
   // ---- copies
   Cursor ahead = cur;
-  int64_t ti = t0;   // the next step to copy
-  int page = -1;     // its page, looked up one step before it is needed
-  uint32_t bad = 0;  // stages whose page lies outside the pool
-  auto look = [&]() {
-    if (ti >= t1) return;
-    seek(ahead, s, a, ti);
-    const int key = (ahead.q.s0 + (int)(ti - ahead.base)) * KSTEP;
-    page = a.table[(int64_t)ahead.b * s.max_pages + (key >> a.shift)];
+  int64_t left = t1 - t0;  // steps still to copy
+  int akey, aleft, ahk;    // the next one's first key, the steps left of its unit, its key/value head
+  const int32_t* arow;     // its row of the block table
+  int page;                // its page, looked up one step before it is needed
+  uint32_t bad = 0;        // stages whose page lies outside the pool
+  auto enter = [&](int64_t t) {  // the copies reach step t of unit `ahead`
+    akey = (ahead.q.s0 + (int)(t - ahead.base)) * KSTEP;
+    aleft = ahead.q.n - (int)(t - ahead.base);
+    ahk = ahead.hu / groups;
+    arow = a.table + (int64_t)ahead.b * s.max_pages;
   };
+  enter(t0);
+  page = arow[akey >> a.shift];
   const uint32_t stage0 = smem_u32(stages);
+  // a lane's i-th piece of a step's K or V lies 512 i bytes on, and goes to 512 i + put[i % PUTS]
+  constexpr int PUTS = CPR / 4;
+  uint32_t put[PUTS];
+#pragma unroll
+  for (int i = 0; i < PUTS; ++i) {
+    const int x = i * 32 + lane;
+    put[i] = piece<T, HD>(x / CPR, x % CPR) - 512 * i;
+  }
   auto issue = [&](int st) {
-    if (ti < t1) {
-      const int key = (ahead.q.s0 + (int)(ti - ahead.base)) * KSTEP;
-      const int hk = ahead.hu / groups;
+    if (left > 0) {
       const bool ok = page >= 0 && page < s.num_pages;
       // keys [from, to) of the step lie in the cache; the new entry (position p) does not
-      const int from = ok ? ahead.q.lo - key : KSTEP, to = ok ? ahead.q.p - key : 0;
-      const int64_t e = ((((int64_t)(ok ? page : 0) * s.Hkv + hk) << a.shift) + (key & (s.page_size - 1))) * HD;
+      const int from = ok ? ahead.q.lo - akey : KSTEP, to = ok ? ahead.q.p - akey : 0;
+      const int64_t e = ((((int64_t)(ok ? page : 0) * s.Hkv + ahk) << a.shift) + (akey & (s.page_size - 1))) * HD +
+                        lane * (16 / (int)sizeof(T));
       const char* gk = reinterpret_cast<const char*>(kp + e);
       const char* gv = reinterpret_cast<const char*>(vp + e);
-      const uint32_t dk = stage0 + st * 2 * KV, dv = dk + KV;
+      const uint32_t dk = stage0 + st * 2 * KV;
       if (from <= 0 && to >= KSTEP) {
 #pragma unroll
         for (int i = 0; i < KSTEP * CPR / 32; ++i) {
-          const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
-          copy16(dk + piece<T, HD>(r, c), gk + x * 16, 16);
-          copy16(dv + piece<T, HD>(r, c), gv + x * 16, 16);
+          copy16(dk + put[i % PUTS] + 512 * i, gk + 512 * i, 16);
+          copy16(dk + put[i % PUTS] + 512 * i + KV, gv + 512 * i, 16);
         }
       } else {
         for (int i = 0; i < KSTEP * CPR / 32; ++i) {
-          const int x = i * 32 + lane, r = x / CPR, c = x % CPR;
+          const int x = i * 32 + lane, r = x / CPR;
           const int bytes = r >= from && r < to ? 16 : 0;
-          copy16(dk + piece<T, HD>(r, c), gk + x * 16, bytes);
-          copy16(dv + piece<T, HD>(r, c), gv + x * 16, bytes);
+          copy16(dk + piece<T, HD>(r, x % CPR), gk + 512 * i, bytes);
+          copy16(dk + piece<T, HD>(r, x % CPR) + KV, gv + 512 * i, bytes);
         }
       }
       bad = ok ? bad & ~(1u << st) : bad | (1u << st);
       if (!ok && lane == 0) record_error(a.err, DEV_BOUNDS);
-      ++ti;
-      look();
+      akey += KSTEP;
+      if (--left > 0) {
+        if (--aleft == 0) {
+          const int64_t next = ahead.base + ahead.q.n;
+          seek(ahead, s, a, next);
+          enter(next);
+        }
+        page = arow[akey >> a.shift];
+      }
     }
     copy_commit();
   };
@@ -639,7 +666,6 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     for (int r = 0; r < NP; ++r) turn[lane + 32 * r] = rope_turn(c.q.p, rf.turns[lane + 32 * r]);
     __syncwarp();
   };
-  look();
   turn_to(cur);  // while the first page number is on its way
 #pragma unroll
   for (int st = 0; st < STAGES; ++st) issue(st);
@@ -715,8 +741,11 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
       }
       __syncwarp();
     }
-    for (; t < end; ++t) {
-      const int key = (cur.q.s0 + (int)(t - cur.base)) * KSTEP;
+    int key = (cur.q.s0 + (int)(t - cur.base)) * KSTEP;
+    const int key_end = key + (int)(end - t) * KSTEP;
+    t = end;
+#pragma unroll 1
+    for (; key < key_end; key += KSTEP) {
       const uint32_t ks = stage0 + st * 2 * KV, vs = ks + KV;
       copy_wait<STAGES - 1>();
       __syncwarp();
