@@ -462,11 +462,16 @@ struct DecodeArgs {
 };
 
 constexpr int PART_M = 128, PART_ROW = 132;  // a part's row: up to 128 channels, then m and l
+// A unit counts as this many steps more than it has keys for: its query and new
+// entry cost a warp about a step's time, and a warp dealt only short units ended
+// last (64 sequences of 64 to 4096: 108 us against 96 on average).
+constexpr int UNIT_COST = 1;
 constexpr int MIN_STEPS = 1;                               // fewest steps of a warp's range
 
-// Steps of one unit of sequence b (0: not running), its position, first key, first step.
+// Position, first key, first step and cost of one unit of sequence b (cost 0: not
+// running). Its steps are the last cost - UNIT_COST of the cost's.
 struct Sequence {
-  int p, lo, s0, n;
+  int p, lo, s0, cost;
 };
 __device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeArgs& a, int b) {
   Sequence r{0, 0, 0, 0};
@@ -475,21 +480,21 @@ __device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeAr
   r.p = (int)p;
   r.lo = s.window > 0 && p >= s.window ? (int)p - s.window + 1 : 0;
   r.s0 = r.lo / KSTEP;
-  r.n = r.p / KSTEP - r.s0 + 1;
+  r.cost = r.p / KSTEP - r.s0 + 1 + UNIT_COST;
   return r;
 }
 
-// Where the global steps lie, from the positions alone: every block of both
-// kernels forms the same sums. Thread i covers `chunk` sequences from i * chunk.
+// The costs of all units in order make one line, which is cut into equal ranges.
+// It follows from the positions alone: every block of both kernels forms the same sums. Thread i covers `chunk` sequences from i * chunk.
 template <int THREADS>
 struct Plan {
-  int64_t before[THREADS];  // steps (of one unit each) of the sequences before thread i's
+  int64_t before[THREADS];  // costs (of one unit each) of the sequences before thread i's
   int64_t sums[THREADS / 32];
-  int owner[THREADS / 32];  // the thread whose sequences hold the first step of the block's warp w
+  int owner[THREADS / 32];  // the thread whose sequences hold where the block's warp w begins
 };
 // What a thread keeps of it.
 struct Steps {
-  int64_t total, per;  // steps of all units, of a warp's range
+  int64_t total, per;  // cost of all units, of a warp's range
   int chunk;
 };
 template <int THREADS>
@@ -498,7 +503,7 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape
   Steps r;
   r.chunk = (s.B + THREADS - 1) / THREADS;
   int64_t mine = 0;
-  for (int b = tid * r.chunk; b < (tid + 1) * r.chunk && b < s.B; ++b) mine += sequence(s, a, b).n;
+  for (int b = tid * r.chunk; b < (tid + 1) * r.chunk && b < s.B; ++b) mine += sequence(s, a, b).cost;
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -531,13 +536,13 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape
   return r;
 }
 
-// The unit that a global step lies in: sequence, unit within it, its first step.
+// The unit that a place on the line lies in: sequence, unit within it, where it begins.
 struct Cursor {
   int b, hu;
   Sequence q;
   int64_t base;
 };
-// The one of step t, which thread `owner`'s sequences hold.
+// The one of place t, which thread `owner`'s sequences hold.
 template <int THREADS>
 __device__ __forceinline__ Cursor locate(const Plan<THREADS>& plan, const Steps& steps, const PagedShape& s,
                                          const DecodeArgs& a, int owner, int64_t t) {
@@ -546,26 +551,23 @@ __device__ __forceinline__ Cursor locate(const Plan<THREADS>& plan, const Steps&
   int64_t at = plan.before[owner] * a.units;
   for (;; ++c.b) {
     c.q = sequence(s, a, c.b);
-    if (t < at + (int64_t)c.q.n * a.units) break;
-    at += (int64_t)c.q.n * a.units;
+    if (t < at + (int64_t)c.q.cost * a.units) break;
+    at += (int64_t)c.q.cost * a.units;
   }
   const int64_t rest = t - at;
-  c.hu = (int)((float)rest / (float)c.q.n);  // off by one at most: units are few
-  if ((int64_t)c.hu * c.q.n > rest) --c.hu;
-  if ((int64_t)(c.hu + 1) * c.q.n <= rest) ++c.hu;
-  c.base = at + (int64_t)c.hu * c.q.n;
+  c.hu = (int)((float)rest / (float)c.q.cost);  // off by one at most: units are few
+  if ((int64_t)c.hu * c.q.cost > rest) --c.hu;
+  if ((int64_t)(c.hu + 1) * c.q.cost <= rest) ++c.hu;
+  c.base = at + (int64_t)c.hu * c.q.cost;
   return c;
 }
-// Moves on to the unit of a later step.
-__device__ __forceinline__ void seek(Cursor& c, const PagedShape& s, const DecodeArgs& a, int64_t t) {
-  while (t >= c.base + c.q.n) {
-    c.base += c.q.n;
-    if (++c.hu == a.units) {
-      c.hu = 0;
-      do c.q = sequence(s, a, ++c.b);
-      while (c.q.n == 0);
-    }
-  }
+// Moves on to the next unit.
+__device__ __forceinline__ void next_unit(Cursor& c, const PagedShape& s, const DecodeArgs& a) {
+  c.base += c.q.cost;
+  if (++c.hu < a.units) return;
+  c.hu = 0;
+  do c.q = sequence(s, a, ++c.b);
+  while (c.q.cost == 0);
 }
 
 template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
@@ -594,21 +596,25 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
   if (t0 >= t1) return;
   const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;  // units, query heads of a key/value head
   Cursor cur = locate(plan, steps, s, a, plan.owner[warp], t0);  // the unit being worked on
+  // [begin, end) of a unit's steps lie in the range
+  auto begin_of = [&](const Cursor& c) { return c.base + UNIT_COST > t0 ? c.base + UNIT_COST : t0; };
+  auto end_of = [&](const Cursor& c) { return c.base + c.q.cost < t1 ? c.base + c.q.cost : t1; };
+  if (begin_of(cur) >= t1) return;  // the last unit's steps are the next warp's
 
   // ---- copies
   Cursor ahead = cur;
-  int64_t left = t1 - t0;  // steps still to copy
-  int akey, aleft, ahk;    // the next one's first key, the steps left of its unit, its key/value head
+  int akey, aleft, ahk;    // the next step's first key, the steps left of its unit (0: of the range), its key/value head
   const int32_t* arow;     // its row of the block table
   int page;                // its page, looked up one step before it is needed
   uint32_t bad = 0;        // stages whose page lies outside the pool
-  auto enter = [&](int64_t t) {  // the copies reach step t of unit `ahead`
-    akey = (ahead.q.s0 + (int)(t - ahead.base)) * KSTEP;
-    aleft = ahead.q.n - (int)(t - ahead.base);
+  auto enter = [&]() {     // the copies reach unit `ahead`
+    const int64_t t = begin_of(ahead);
+    akey = (ahead.q.s0 + (int)(t - ahead.base - UNIT_COST)) * KSTEP;
+    aleft = (int)(end_of(ahead) - t);
     ahk = ahead.hu / groups;
     arow = a.table + (int64_t)ahead.b * s.max_pages;
   };
-  enter(t0);
+  enter();
   page = arow[akey >> a.shift];
   const uint32_t stage0 = smem_u32(stages);
   // a lane's i-th piece of a step's K or V lies 512 i bytes on, and goes to 512 i + put[i % PUTS]
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     put[i] = piece<T, HD>(x / CPR, x % CPR) - 512 * i;
   }
   auto issue = [&](int st) {
-    if (left > 0) {
+    if (aleft > 0) {
       const bool ok = page >= 0 && page < s.num_pages;
       // keys [from, to) of the step lie in the cache; the new entry (position p) does not
       const int from = ok ? ahead.q.lo - akey : KSTEP, to = ok ? ahead.q.p - akey : 0;
@@ -646,14 +652,11 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
       bad = ok ? bad & ~(1u << st) : bad | (1u << st);
       if (!ok && lane == 0) record_error(a.err, DEV_BOUNDS);
       akey += KSTEP;
-      if (--left > 0) {
-        if (--aleft == 0) {
-          const int64_t next = ahead.base + ahead.q.n;
-          seek(ahead, s, a, next);
-          enter(next);
-        }
-        page = arow[akey >> a.shift];
+      if (--aleft == 0 && ahead.base + ahead.q.cost + UNIT_COST < t1) {
+        next_unit(ahead, s, a);
+        enter();
       }
+      if (aleft > 0) page = arow[akey >> a.shift];
     }
     copy_commit();
   };
@@ -673,13 +676,12 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
   // ---- the range's units in order
   Tile tile;
   int st = 0;
-  for (int64_t t = t0; t < t1;) {
-    seek(cur, s, a, t);
-    const int64_t end = cur.base + cur.q.n < t1 ? cur.base + cur.q.n : t1;  // steps [t, end) of the unit
+  for (;;) {
+    const int64_t t = begin_of(cur), end = end_of(cur);  // steps [t, end) of the unit
     const int hk = cur.hu / groups;
     const int h0 = hk * per_kv + (cur.hu % groups) * a.heads;
     const int heads = min(a.heads, (hk + 1) * per_kv - h0);
-    const bool has_new = end == cur.base + cur.q.n, whole = t == cur.base && has_new, first = t == t0;
+    const bool has_new = end == cur.base + cur.q.cost, whole = t == cur.base + UNIT_COST && has_new;
     // every load of the unit at once: the query rows, and the new entry's parts
     const int64_t row = ((int64_t)cur.b * s.Hkv + hk) * HD;
     float k1[NP], k2[NP], v1[NP], v2[NP], kr1[NP], kr2[NP], vr1[NP], vr2[NP], ga = 0.f, gb = 0.f, gc = 0.f, gd = 0.f;
@@ -741,9 +743,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
       }
       __syncwarp();
     }
-    int key = (cur.q.s0 + (int)(t - cur.base)) * KSTEP;
+    int key = (cur.q.s0 + (int)(t - cur.base - UNIT_COST)) * KSTEP;
     const int key_end = key + (int)(end - t) * KSTEP;
-    t = end;
 #pragma unroll 1
     for (; key < key_end; key += KSTEP) {
       const uint32_t ks = stage0 + st * 2 * KV, vs = ks + KV;
@@ -773,13 +774,16 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
           heads, [](float l) { return l == 0.f ? 0.f : 1.f / l; },
           [&](int j, int c, float x) { d[j * HD + c] = from_f<T>(x); });
     } else {
-      float* part = a.parts + ((int64_t)me * 2 + (first ? 0 : 1)) * a.heads * PART_ROW;
+      // the unit that holds the range's first place, or the one that goes on behind its last
+      float* part = a.parts + ((int64_t)me * 2 + (cur.base + UNIT_COST <= t0 ? 0 : 1)) * a.heads * PART_ROW;
       tile.each_out(
           heads, [](float) { return 1.f; }, [&](int j, int c, float x) { part[j * PART_ROW + c] = x; });
       tile.each_head(heads, [&](int j, float m, float l) {
         *reinterpret_cast<float2*>(part + j * PART_ROW + PART_M) = make_float2(m, l);
       });
     }
+    if (cur.base + cur.q.cost + UNIT_COST >= t1) break;
+    next_unit(cur, s, a);
   }
 }
 
@@ -807,12 +811,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedShape s, 
   const int hk = h / per_kv, in_kv = h - hk * per_kv, j = in_kv % a.heads;
   const int i = b / steps.chunk;
   int64_t base = plan.before[i];
-  for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).n;
-  base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.n;  // the unit's first step
+  for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
+  base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;  // the unit's first step
   const int64_t per = steps.per;
-  const int w0 = (int)(base / per), np = q.n ? (int)((base + q.n - 1) / per) - w0 + 1 : 0;  // warps with a part
+  // warps with a part
+  const int w0 = (int)(base / per), np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / per) - w0 + 1 : 0;
   const int64_t stride = (int64_t)2 * a.heads * PART_ROW;
-  // warp w0's part may follow other units in its range; the others begin with this unit
+  // warp w0's part may follow other units in its range; the other warps begin with this unit
   const float* part = a.parts + w0 * stride + j * PART_ROW;
   auto part_of = [&](int x) { return part + x * stride + (x == 0 && base > per * w0 ? stride / 2 : 0); };
   T* out = static_cast<T*>(a.out) + pair * HD;
@@ -910,7 +915,7 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   // steps there can be at most, from the sizes alone
   int64_t keys = (int64_t)s.max_pages * s.page_size;
   if (s.window > 0 && s.window + KSTEP < keys) keys = s.window + KSTEP;
-  const int64_t steps = (keys + KSTEP - 1) / KSTEP * a.units * s.B;
+  const int64_t steps = ((keys + KSTEP - 1) / KSTEP + UNIT_COST) * a.units * s.B;
   const int64_t most = (steps + NW * MIN_STEPS - 1) / (NW * MIN_STEPS);
   constexpr size_t smem = (size_t)NW * (STAGES * 2 * KSTEP * HD * sizeof(T) + Tile::WARP_BYTES + 2 * HD * sizeof(T) +
                                         HD / 2 * sizeof(float2));
