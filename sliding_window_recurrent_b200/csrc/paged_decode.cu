@@ -259,18 +259,24 @@ struct MmaTile {
     }
   }
   // sums over the lanes that share a head
-  __device__ __forceinline__ void finish() {
+  __device__ __forceinline__ void finish(int heads) {
 #pragma unroll
     for (int n = 0; n < NH; ++n) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
-      if (ONE) {
+      if (ONE) {  // upper and lower parts; a single head lies in the even columns
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[k][n][e] += __shfl_xor_sync(0xffffffffu, o[k][n][e], 2);
+          for (int e = 0; e < 4; e += 2) o[k][n][e] += __shfl_xor_sync(0xffffffffu, o[k][n][e], 2);
+        if (heads > 1) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 1; e < 4; e += 2) o[k][n][e] += __shfl_xor_sync(0xffffffffu, o[k][n][e], 2);
+        }
       }
     }
   }
@@ -412,7 +418,7 @@ struct SimtTile {
         }
     }
   }
-  __device__ __forceinline__ void finish() {
+  __device__ __forceinline__ void finish(int) {
 #pragma unroll
     for (int j = 0; j < HEADS; ++j) {
 #pragma unroll
@@ -465,7 +471,7 @@ constexpr int PART_M = 128, PART_ROW = 132;  // a part's row: up to 128 channels
 // A unit counts as this many steps more than it has keys for: its query and new
 // entry cost a warp about a step's time, and a warp dealt only short units ended
 // last (64 sequences of 64 to 4096: 108 us against 96 on average).
-constexpr int UNIT_COST = 1;
+constexpr int UNIT_COST = 3;
 constexpr int MIN_STEPS = 1;                               // fewest steps of a warp's range
 
 // Position, first key, first step and cost of one unit of sequence b (cost 0: not
@@ -473,15 +479,18 @@ constexpr int MIN_STEPS = 1;                               // fewest steps of a 
 struct Sequence {
   int p, lo, s0, cost;
 };
-__device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeArgs& a, int b) {
+__device__ __forceinline__ Sequence sequence_at(const PagedShape& s, const DecodeArgs& a, int64_t p) {
   Sequence r{0, 0, 0, 0};
-  const int64_t p = a.pos[b];
   if (p < 0 || p >= (int64_t)s.max_pages << a.shift) return r;
   r.p = (int)p;
   r.lo = s.window > 0 && p >= s.window ? (int)p - s.window + 1 : 0;
   r.s0 = r.lo / KSTEP;
   r.cost = r.p / KSTEP - r.s0 + 1 + UNIT_COST;
   return r;
+}
+
+__device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeArgs& a, int b) {
+  return sequence_at(s, a, a.pos[b]);
 }
 
 // The costs of all units in order make one line, which is cut into equal ranges.
@@ -503,7 +512,14 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape
   Steps r;
   r.chunk = (s.B + THREADS - 1) / THREADS;
   int64_t mine = 0;
-  for (int b = tid * r.chunk; b < (tid + 1) * r.chunk && b < s.B; ++b) mine += sequence(s, a, b).cost;
+  const int b0 = tid * r.chunk, b1 = b0 + r.chunk < s.B ? b0 + r.chunk : s.B;
+  for (int b = b0; b < b1; b += 8) {
+    int64_t p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p[e] = b + e < b1 ? a.pos[b + e] : -1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine += sequence_at(s, a, p[e]).cost;
+  }
   int64_t inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -767,7 +783,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
       issue(st);
       st = st + 1 == STAGES ? 0 : st + 1;
     }
-    tile.finish();
+    tile.finish(heads);
     if (whole) {
       T* d = out + ((int64_t)cur.b * s.H + h0) * HD;
       tile.each_out(
@@ -796,103 +812,109 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
 constexpr int JOIN_THREADS = 256;
 
 template <typename T, int HD, int JW>
-__global__ void __launch_bounds__(JOIN_THREADS) paged_join_kernel(PagedShape s, DecodeArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS, 2) paged_join_kernel(PagedShape s, DecodeArgs a) {
   constexpr int NW = JOIN_THREADS / 32, V = HD / 4, LANES = 32 / V;  // lanes that share four channels (hd 64: 2)
   __shared__ Plan<JOIN_THREADS> plan;
   __shared__ float4 so[NW][V];
   __shared__ float sm[NW], sl[NW];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Steps steps = form_plan(plan, s, a);  // reads nothing that the first kernel writes
-  const int64_t pair = (int64_t)blockIdx.x * (NW / JW) + warp / JW;
-  const bool in = pair < (int64_t)s.B * s.H;
-  const int b = in ? (int)(pair / s.H) : 0, h = in ? (int)(pair % s.H) : 0;
-  const Sequence q = sequence(s, a, b);
-  const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
-  const int hk = h / per_kv, in_kv = h - hk * per_kv, j = in_kv % a.heads;
-  const int i = b / steps.chunk;
-  int64_t base = plan.before[i];
-  for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
-  base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;  // the unit's first step
-  const int64_t per = steps.per;
-  // warps with a part
-  const int w0 = (int)(base / per), np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / per) - w0 + 1 : 0;
-  const int64_t stride = (int64_t)2 * a.heads * PART_ROW;
-  // warp w0's part may follow other units in its range; the other warps begin with this unit
-  const float* part = a.parts + w0 * stride + j * PART_ROW;
-  auto part_of = [&](int x) { return part + x * stride + (x == 0 && base > per * w0 ? stride / 2 : 0); };
-  T* out = static_cast<T*>(a.out) + pair * HD;
-  const int c = lane % V * 4;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (np > 1) {
-    const int step = JW * LANES, x1 = (warp % JW) * LANES + lane / V;
+  const int64_t pairs = (int64_t)s.B * s.H, per_round = (int64_t)gridDim.x * (NW / JW);
+  bool waited = false;
+  for (int64_t first = (int64_t)blockIdx.x * (NW / JW); first < pairs; first += per_round) {
+    const int64_t pair = first + warp / JW;
+    const bool in = pair < pairs;
+    const int b = in ? (int)(pair / s.H) : 0, h = in ? (int)(pair % s.H) : 0;
+    const Sequence q = sequence(s, a, b);
+    const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
+    const int hk = h / per_kv, in_kv = h - hk * per_kv, j = in_kv % a.heads;
+    const int i = b / steps.chunk;
+    int64_t base = plan.before[i];
+    for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
+    base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;  // the unit's first step
+    const int64_t per = steps.per;
+    // warps with a part
+    const int w0 = (int)(base / per), np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / per) - w0 + 1 : 0;
+    const int64_t stride = (int64_t)2 * a.heads * PART_ROW;
+    // warp w0's part may follow other units in its range; the other warps begin with this unit
+    const float* part = a.parts + w0 * stride + j * PART_ROW;
+    auto part_of = [&](int x) { return part + x * stride + (x == 0 && base > per * w0 ? stride / 2 : 0); };
+    T* out = static_cast<T*>(a.out) + pair * HD;
+    const int c = lane % V * 4;
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+    waited = true;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (np > 1) {
+      const int step = JW * LANES, x1 = (warp % JW) * LANES + lane / V;
 #pragma unroll 1
-    for (int x0 = x1; x0 < np; x0 += 16 * step) {
-      float2 ml[16];
-      float4 y[16];
+      for (int x0 = x1; x0 < np; x0 += 16 * step) {
+        float2 ml[16];
+        float4 y[16];
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        const int x = x0 + u * step;
-        ml[u] = make_float2(-INFINITY, 0.f);
-        if (x < np) {
-          ml[u] = __ldcg(reinterpret_cast<const float2*>(part_of(x) + PART_M));
-          y[u] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + c));
+        for (int u = 0; u < 16; ++u) {
+          const int x = x0 + u * step;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          if (x < np) {
+            ml[u] = __ldcg(reinterpret_cast<const float2*>(part_of(x) + PART_M));
+            y[u] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + c));
+          }
+        }
+        float mn = m;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) mn = fmaxf(mn, ml[u].x);
+        const float r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r);
+        l *= f;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+        m = mn;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          if (x0 + u * step >= np) break;
+          const float w = pow2(ml[u].x - r);
+          l += w * ml[u].y;
+          o.x += w * y[u].x;
+          o.y += w * y[u].y;
+          o.z += w * y[u].z;
+          o.w += w * y[u].w;
         }
       }
-      float mn = m;
-#pragma unroll
-      for (int u = 0; u < 16; ++u) mn = fmaxf(mn, ml[u].x);
-      const float r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r);
-      l *= f;
-      o.x *= f;
-      o.y *= f;
-      o.z *= f;
-      o.w *= f;
+    }
+    auto add = [&](float m2, float l2, float4 o2) {  // another set of parts
+      const float mn = fmaxf(m, m2), r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r), f2 = pow2(m2 - r);
+      l = l * f + l2 * f2;
+      o.x = o.x * f + o2.x * f2;
+      o.y = o.y * f + o2.y * f2;
+      o.z = o.z * f + o2.z * f2;
+      o.w = o.w * f + o2.w * f2;
       m = mn;
-#pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        if (x0 + u * step >= np) break;
-        const float w = pow2(ml[u].x - r);
-        l += w * ml[u].y;
-        o.x += w * y[u].x;
-        o.y += w * y[u].y;
-        o.z += w * y[u].z;
-        o.w += w * y[u].w;
+    };
+    if (LANES > 1) {
+      const float4 y = make_float4(__shfl_down_sync(0xffffffffu, o.x, 16), __shfl_down_sync(0xffffffffu, o.y, 16),
+                                   __shfl_down_sync(0xffffffffu, o.z, 16), __shfl_down_sync(0xffffffffu, o.w, 16));
+      add(__shfl_down_sync(0xffffffffu, m, 16), __shfl_down_sync(0xffffffffu, l, 16), y);
+    }
+    if (JW > 1) {
+      __syncthreads();  // the last round's have been read
+      if (lane < V) so[warp][lane] = o;
+      if (lane == 0) {
+        sm[warp] = m;
+        sl[warp] = l;
       }
+      __syncthreads();
+      if (warp % JW == 0 && lane < V)
+        for (int w = 1; w < JW; ++w) add(sm[warp + w], sl[warp + w], so[warp + w][lane]);
     }
+    if (!in || np == 1 || warp % JW != 0 || lane >= V) continue;  // np == 1: its warp has written it
+    if (np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
+    const float f = l == 0.f ? 0.f : 1.f / l;
+    out[c] = from_f<T>(o.x * f);
+    out[c + 1] = from_f<T>(o.y * f);
+    out[c + 2] = from_f<T>(o.z * f);
+    out[c + 3] = from_f<T>(o.w * f);
   }
-  auto add = [&](float m2, float l2, float4 o2) {  // another set of parts
-    const float mn = fmaxf(m, m2), r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r), f2 = pow2(m2 - r);
-    l = l * f + l2 * f2;
-    o.x = o.x * f + o2.x * f2;
-    o.y = o.y * f + o2.y * f2;
-    o.z = o.z * f + o2.z * f2;
-    o.w = o.w * f + o2.w * f2;
-    m = mn;
-  };
-  if (LANES > 1) {
-    const float4 y = make_float4(__shfl_down_sync(0xffffffffu, o.x, 16), __shfl_down_sync(0xffffffffu, o.y, 16),
-                                 __shfl_down_sync(0xffffffffu, o.z, 16), __shfl_down_sync(0xffffffffu, o.w, 16));
-    add(__shfl_down_sync(0xffffffffu, m, 16), __shfl_down_sync(0xffffffffu, l, 16), y);
-  }
-  if (JW > 1) {
-    if (lane < V) so[warp][lane] = o;
-    if (lane == 0) {
-      sm[warp] = m;
-      sl[warp] = l;
-    }
-    __syncthreads();
-    if (warp % JW == 0 && lane < V)
-      for (int w = 1; w < JW; ++w) add(sm[warp + w], sl[warp + w], so[warp + w][lane]);
-  }
-  if (!in || np == 1 || warp % JW != 0 || lane >= V) return;  // np == 1: its warp has written it
-  if (np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
-  const float f = l == 0.f ? 0.f : 1.f / l;
-  out[c] = from_f<T>(o.x * f);
-  out[c + 1] = from_f<T>(o.y * f);
-  out[c + 2] = from_f<T>(o.z * f);
-  out[c + 3] = from_f<T>(o.w * f);
 }
 
 int units_of(const PagedShape& s, int heads) {  // units of a sequence
@@ -934,9 +956,10 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   const int64_t pairs = (int64_t)s.B * s.H;
   const bool many = (int64_t)s.B * a.units * 4 >= a.warps;  // a few parts to a unit: a warp joins them alone
   const int per_block = JOIN_THREADS / 32 / (many ? 1 : 8);
-  const unsigned blocks = (unsigned)((pairs + per_block - 1) / per_block);
-  return many ? launch_dependent(paged_join_kernel<T, HD, 1>, blocks, JOIN_THREADS, st, s, a)
-              : launch_dependent(paged_join_kernel<T, HD, 8>, blocks, JOIN_THREADS, st, s, a);
+  int64_t blocks = (pairs + per_block - 1) / per_block;
+  if (blocks > 2 * num_sms()) blocks = 2 * num_sms();
+  return many ? launch_dependent(paged_join_kernel<T, HD, 1>, (unsigned)blocks, JOIN_THREADS, st, s, a)
+              : launch_dependent(paged_join_kernel<T, HD, 8>, (unsigned)blocks, JOIN_THREADS, st, s, a);
 }
 
 }  // namespace
