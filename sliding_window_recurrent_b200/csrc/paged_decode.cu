@@ -7,15 +7,16 @@
 // every entry (window 0).
 //
 // Mathematics. For a query row q (rotated, scaled to log2 units) and any split of
-// its keys into parts, each part keeps (m, l, o): a reference m >= is not needed
-// to be the exact maximum, l = sum 2^(s_j - m), o = sum 2^(s_j - m) v_j. Parts join
-// by M = max m_i, l = sum 2^(m_i - M) l_i, o likewise, out = o / l.
+// its keys into parts, each part keeps (m, l, o): a reference m near the maximum
+// of its scores s_j, l = sum 2^(s_j - m), o = sum 2^(s_j - m) v_j. Parts join by
+// M = max m_i, l = sum 2^(m_i - M) l_i, o likewise, out = o / l.
 //
 // Split. The cache is read once and nothing else is large, so the kernel is bound
 // by HBM and has to keep every SM streaming whatever the lengths are. A unit is a
 // (sequence, key/value head, group of query heads) and is cut into steps of 16
 // keys (a page holds a whole number of steps). All steps of all units, in order,
-// are dealt to the warps of the grid in equal contiguous ranges. A warp works
+// are dealt to the warps of the grid in equal contiguous ranges (a unit weighs a few
+// steps more than it has, for its query and its end). A warp works
 // alone: it streams its steps through its own ring of shared-memory stages
 // (16-byte asynchronous copies that run ahead across units), keeps (m, l, o) in
 // registers, writes the outputs of units that lie in its range, and leaves parts
@@ -468,11 +469,12 @@ struct DecodeArgs {
 };
 
 constexpr int PART_M = 128, PART_ROW = 132;  // a part's row: up to 128 channels, then m and l
-// A unit counts as this many steps more than it has keys for: its query and new
-// entry cost a warp about a step's time, and a warp dealt only short units ended
-// last (64 sequences of 64 to 4096: 108 us against 96 on average).
+// A unit counts as this many steps more than it has: its query, its new entry and
+// its end keep a warp from its copies for about that time, and a warp dealt only
+// short units ended last (64 sequences of 64 to 4096: 108 us, 96 on average; 512
+// of up to 190: 72, 66, 61, 61 us in all with 1, 2, 3, 4).
 constexpr int UNIT_COST = 3;
-constexpr int MIN_STEPS = 1;                               // fewest steps of a warp's range
+constexpr int MIN_COST = 1;  // least of a warp's range
 
 // Position, first key, first step and cost of one unit of sequence b (cost 0: not
 // running). Its steps are the last cost - UNIT_COST of the cost's.
@@ -494,7 +496,8 @@ __device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeAr
 }
 
 // The costs of all units in order make one line, which is cut into equal ranges.
-// It follows from the positions alone: every block of both kernels forms the same sums. Thread i covers `chunk` sequences from i * chunk.
+// It follows from the positions alone: every block of both kernels forms the same
+// sums. Thread i covers `chunk` sequences from i * chunk.
 template <int THREADS>
 struct Plan {
   int64_t before[THREADS];  // costs (of one unit each) of the sequences before thread i's
@@ -540,7 +543,7 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape
   // total / warps, rounded up (a 64-bit division would take 0.3 us here)
   r.per = r.total > 0 ? (int64_t)((double)(r.total - 1) * a.inv_warps) + 1 : 1;
   if (r.per * a.warps < r.total) ++r.per;
-  if (r.per < MIN_STEPS) r.per = MIN_STEPS;
+  if (r.per < MIN_COST) r.per = MIN_COST;
   at *= a.units;
   mine *= a.units;
 #pragma unroll
@@ -805,115 +808,145 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
 
 // ---------------------------------------------------------------------------
 // The outputs of units in several warps' ranges, and zeros for sequences that are
-// not running. JW warps take a (sequence, query head) together: a lane owns four
-// channels, the warps deal the parts among them, and sixteen loads a lane are in
-// flight (what counts is the latency of parts that lie in L2).
+// not running. A warp takes a (sequence, query head); where the head has more parts
+// than a warp has in flight, its block's warps take it together. A lane owns four
+// channels: what counts is the latency of parts in L2.
 // ---------------------------------------------------------------------------
-constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_WARPS = 8;
+constexpr int FLY = 8;  // parts of a lane in flight
 
-template <typename T, int HD, int JW>
-__global__ void __launch_bounds__(JOIN_THREADS, 2) paged_join_kernel(PagedShape s, DecodeArgs a) {
-  constexpr int NW = JOIN_THREADS / 32, V = HD / 4, LANES = 32 / V;  // lanes that share four channels (hd 64: 2)
-  __shared__ Plan<JOIN_THREADS> plan;
+// (m, l, o) of four channels over some of a unit's parts.
+struct Joined {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void add(float m2, float l2, float4 o2) {
+    const float mn = fmaxf(m, m2), r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r), f2 = pow2(m2 - r);
+    l = l * f + l2 * f2;
+    o.x = o.x * f + o2.x * f2;
+    o.y = o.y * f + o2.y * f2;
+    o.z = o.z * f + o2.z * f2;
+    o.w = o.w * f + o2.w * f2;
+    m = mn;
+  }
+};
+// Where the parts of a head lie: the first one, the others `stride` apart from `rest` on.
+struct Parts {
+  const float *first, *rest;
+  int np;
+};
+
+// Parts x1, x1 + step, ... of a head, channels c..c+3.
+__device__ __forceinline__ Joined join_parts(const Parts& p, int64_t stride, int c, int x1, int step) {
+  Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 1
+  for (int x0 = x1; x0 < p.np; x0 += FLY * step) {
+    float2 ml[FLY];
+    float4 y[FLY];
+#pragma unroll
+    for (int u = 0; u < FLY; ++u) {
+      const int x = x0 + u * step;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (x < p.np) {
+        const float* part = x == 0 ? p.first : p.rest + x * stride;
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(part + PART_M));
+        y[u] = __ldcg(reinterpret_cast<const float4*>(part + c));
+      }
+    }
+    float mn = r.m;
+#pragma unroll
+    for (int u = 0; u < FLY; ++u) mn = fmaxf(mn, ml[u].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, f = pow2(r.m - ref);
+    r.l *= f;
+    r.o.x *= f;
+    r.o.y *= f;
+    r.o.z *= f;
+    r.o.w *= f;
+    r.m = mn;
+#pragma unroll
+    for (int u = 0; u < FLY; ++u) {
+      if (x0 + u * step >= p.np) break;
+      const float w = pow2(ml[u].x - ref);
+      r.l += w * ml[u].y;
+      r.o.x += w * y[u].x;
+      r.o.y += w * y[u].y;
+      r.o.z += w * y[u].z;
+      r.o.w += w * y[u].w;
+    }
+  }
+  return r;
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedShape s, DecodeArgs a, int per_block) {
+  constexpr int NW = JOIN_WARPS, V = HD / 4, SHARE = 32 / V;  // lanes that share four channels (hd 64: 2)
+  constexpr int ALONE = FLY * SHARE;                          // parts that a warp takes alone
+  __shared__ Plan<NW * 32> plan;
+  __shared__ Parts parts[NW];
   __shared__ float4 so[NW][V];
   __shared__ float sm[NW], sl[NW];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % V * 4;
   const Steps steps = form_plan(plan, s, a);  // reads nothing that the first kernel writes
-  const int64_t pairs = (int64_t)s.B * s.H, per_round = (int64_t)gridDim.x * (NW / JW);
+  const int64_t heads = (int64_t)s.B * s.H, stride = (int64_t)2 * a.heads * PART_ROW;  // from warp to warp
+  const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
   bool waited = false;
-  for (int64_t first = (int64_t)blockIdx.x * (NW / JW); first < pairs; first += per_round) {
-    const int64_t pair = first + warp / JW;
-    const bool in = pair < pairs;
-    const int b = in ? (int)(pair / s.H) : 0, h = in ? (int)(pair % s.H) : 0;
-    const Sequence q = sequence(s, a, b);
-    const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
-    const int hk = h / per_kv, in_kv = h - hk * per_kv, j = in_kv % a.heads;
-    const int i = b / steps.chunk;
-    int64_t base = plan.before[i];
-    for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
-    base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;  // the unit's first step
-    const int64_t per = steps.per;
-    // warps with a part
-    const int w0 = (int)(base / per), np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / per) - w0 + 1 : 0;
-    const int64_t stride = (int64_t)2 * a.heads * PART_ROW;
-    // warp w0's part may follow other units in its range; the other warps begin with this unit
-    const float* part = a.parts + w0 * stride + j * PART_ROW;
-    auto part_of = [&](int x) { return part + x * stride + (x == 0 && base > per * w0 ? stride / 2 : 0); };
-    T* out = static_cast<T*>(a.out) + pair * HD;
-    const int c = lane % V * 4;
+  for (int64_t at = (int64_t)blockIdx.x * per_block; at < heads; at += (int64_t)gridDim.x * per_block) {
+    const int64_t head = at + warp;
+    const bool mine = warp < per_block && head < heads;
+    Parts p{nullptr, nullptr, 1};
+    if (mine) {
+      const int b = (int)(head / s.H), h = (int)(head % s.H), hk = h / per_kv, in_kv = h - hk * per_kv;
+      const Sequence q = sequence(s, a, b);
+      const int i = b / steps.chunk;
+      int64_t base = plan.before[i];
+      for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
+      // the unit's first step, and the warps that have steps of it
+      base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;
+      const int w0 = (int)(base / steps.per);
+      p.np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / steps.per) - w0 + 1 : 0;
+      p.rest = a.parts + w0 * stride + in_kv % a.heads * PART_ROW;
+      p.first = p.rest + (base > steps.per * w0 ? stride / 2 : 0);  // behind other units of warp w0's range
+      if (p.np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
+    }
     if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
     waited = true;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (np > 1) {
-      const int step = JW * LANES, x1 = (warp % JW) * LANES + lane / V;
+    // (the barrier also ends the last round's use of the shared rows)
+    const int help = __syncthreads_or(p.np > ALONE) ? per_block : 0;
+    if (help) {
+      if (lane == 0) parts[warp] = p;
+      __syncthreads();
+    }
+    Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 1
-      for (int x0 = x1; x0 < np; x0 += 16 * step) {
-        float2 ml[16];
-        float4 y[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          const int x = x0 + u * step;
-          ml[u] = make_float2(-INFINITY, 0.f);
-          if (x < np) {
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(part_of(x) + PART_M));
-            y[u] = __ldcg(reinterpret_cast<const float4*>(part_of(x) + c));
-          }
-        }
-        float mn = m;
-#pragma unroll
-        for (int u = 0; u < 16; ++u) mn = fmaxf(mn, ml[u].x);
-        const float r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r);
-        l *= f;
-        o.x *= f;
-        o.y *= f;
-        o.z *= f;
-        o.w *= f;
-        m = mn;
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          if (x0 + u * step >= np) break;
-          const float w = pow2(ml[u].x - r);
-          l += w * ml[u].y;
-          o.x += w * y[u].x;
-          o.y += w * y[u].y;
-          o.z += w * y[u].z;
-          o.w += w * y[u].w;
-        }
+    for (int i = 0; i <= help; ++i) {  // the heads with many parts together, then each warp its own
+      const bool together = i < help;
+      if (together ? parts[i].np <= ALONE : p.np == 1 || p.np > ALONE) continue;
+      Joined x = join_parts(together ? parts[i] : p, stride, c, (together ? warp * SHARE : 0) + lane / V,
+                            (together ? NW : 1) * SHARE);
+      if (SHARE > 1)  // lanes with the same channels
+        x.add(__shfl_down_sync(0xffffffffu, x.m, 16), __shfl_down_sync(0xffffffffu, x.l, 16),
+              make_float4(__shfl_down_sync(0xffffffffu, x.o.x, 16), __shfl_down_sync(0xffffffffu, x.o.y, 16),
+                          __shfl_down_sync(0xffffffffu, x.o.z, 16), __shfl_down_sync(0xffffffffu, x.o.w, 16)));
+      if (!together) {
+        r = x;
+        break;
       }
-    }
-    auto add = [&](float m2, float l2, float4 o2) {  // another set of parts
-      const float mn = fmaxf(m, m2), r = mn == -INFINITY ? 0.f : mn, f = pow2(m - r), f2 = pow2(m2 - r);
-      l = l * f + l2 * f2;
-      o.x = o.x * f + o2.x * f2;
-      o.y = o.y * f + o2.y * f2;
-      o.z = o.z * f + o2.z * f2;
-      o.w = o.w * f + o2.w * f2;
-      m = mn;
-    };
-    if (LANES > 1) {
-      const float4 y = make_float4(__shfl_down_sync(0xffffffffu, o.x, 16), __shfl_down_sync(0xffffffffu, o.y, 16),
-                                   __shfl_down_sync(0xffffffffu, o.z, 16), __shfl_down_sync(0xffffffffu, o.w, 16));
-      add(__shfl_down_sync(0xffffffffu, m, 16), __shfl_down_sync(0xffffffffu, l, 16), y);
-    }
-    if (JW > 1) {
-      __syncthreads();  // the last round's have been read
-      if (lane < V) so[warp][lane] = o;
+      if (lane < V) so[warp][lane] = x.o;
       if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
+        sm[warp] = x.m;
+        sl[warp] = x.l;
       }
       __syncthreads();
-      if (warp % JW == 0 && lane < V)
-        for (int w = 1; w < JW; ++w) add(sm[warp + w], sl[warp + w], so[warp + w][lane]);
+      if (warp == i && lane < V)
+        for (int w = 0; w < NW; ++w) r.add(sm[w], sl[w], so[w][lane]);
+      __syncthreads();
     }
-    if (!in || np == 1 || warp % JW != 0 || lane >= V) continue;  // np == 1: its warp has written it
-    if (np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
-    const float f = l == 0.f ? 0.f : 1.f / l;
-    out[c] = from_f<T>(o.x * f);
-    out[c + 1] = from_f<T>(o.y * f);
-    out[c + 2] = from_f<T>(o.z * f);
-    out[c + 3] = from_f<T>(o.w * f);
+    if (!mine || p.np == 1 || lane >= V) continue;  // np == 1: its warp has written it
+    T* out = static_cast<T*>(a.out) + head * HD;
+    const float f = r.l == 0.f ? 0.f : 1.f / r.l;
+    out[c] = from_f<T>(r.o.x * f);
+    out[c + 1] = from_f<T>(r.o.y * f);
+    out[c + 2] = from_f<T>(r.o.z * f);
+    out[c + 3] = from_f<T>(r.o.w * f);
   }
 }
 
@@ -926,7 +959,7 @@ int tile_heads(const PagedShape& s) {
   if (s.dtype == 0) return 4;
   return s.H / s.Hkv > 8 ? 16 : s.H / s.Hkv > 4 ? 8 : 4;
 }
-constexpr int MAX_WARPS = 12;  // of an SM
+constexpr int MAX_WARPS = 12;  // of an SM, at most
 
 template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
 cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
@@ -938,7 +971,7 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   int64_t keys = (int64_t)s.max_pages * s.page_size;
   if (s.window > 0 && s.window + KSTEP < keys) keys = s.window + KSTEP;
   const int64_t steps = ((keys + KSTEP - 1) / KSTEP + UNIT_COST) * a.units * s.B;
-  const int64_t most = (steps + NW * MIN_STEPS - 1) / (NW * MIN_STEPS);
+  const int64_t most = (steps + NW * MIN_COST - 1) / (NW * MIN_COST);
   constexpr size_t smem = (size_t)NW * (STAGES * 2 * KSTEP * HD * sizeof(T) + Tile::WARP_BYTES + 2 * HD * sizeof(T) +
                                         HD / 2 * sizeof(float2));
   static_assert((smem + sizeof(Plan<NW * 32>) + 1024) * OCC <= 228 * 1024, "OCC blocks share an SM's memory");
@@ -953,13 +986,11 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the join: scheduled as the first kernel ends, its blocks wait for that before they read a part
-  const int64_t pairs = (int64_t)s.B * s.H;
-  const bool many = (int64_t)s.B * a.units * 4 >= a.warps;  // a few parts to a unit: a warp joins them alone
-  const int per_block = JOIN_THREADS / 32 / (many ? 1 : 8);
-  int64_t blocks = (pairs + per_block - 1) / per_block;
-  if (blocks > 2 * num_sms()) blocks = 2 * num_sms();
-  return many ? launch_dependent(paged_join_kernel<T, HD, 1>, (unsigned)blocks, JOIN_THREADS, st, s, a)
-              : launch_dependent(paged_join_kernel<T, HD, 8>, (unsigned)blocks, JOIN_THREADS, st, s, a);
+  const int64_t heads = (int64_t)s.B * s.H, blocks = 2 * num_sms();
+  int per_block = (int)((heads + blocks - 1) / blocks < JOIN_WARPS ? (heads + blocks - 1) / blocks : JOIN_WARPS);
+  const int64_t need = (heads + per_block - 1) / per_block;
+  return launch_dependent(paged_join_kernel<T, HD>, (unsigned)(need < blocks ? need : blocks), JOIN_WARPS * 32, st, s, a,
+                          per_block);
 }
 
 }  // namespace
@@ -994,9 +1025,9 @@ cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const v
            : heads == 8 ? run<bf16, 128, MmaTile<128, 2>, 4, 2, 2>(s, a, st)
                         : run<bf16, 128, MmaTile<128, 4>, 4, 2, 2>(s, a, st);
   if (s.dtype == 1 && s.hd == 64)
-    return heads == 4   ? run<bf16, 64, MmaTile<64, 1>, 4, 4, 3>(s, a, st)
-           : heads == 8 ? run<bf16, 64, MmaTile<64, 2>, 4, 4, 3>(s, a, st)
-                        : run<bf16, 64, MmaTile<64, 4>, 4, 4, 2>(s, a, st);
+    return heads == 4   ? run<bf16, 64, MmaTile<64, 1>, 4, 2, 3>(s, a, st)
+           : heads == 8 ? run<bf16, 64, MmaTile<64, 2>, 4, 3, 2>(s, a, st)
+                        : run<bf16, 64, MmaTile<64, 4>, 4, 3, 2>(s, a, st);
   if (s.dtype == 0 && s.hd == 128) return run<float, 128, SimtTile<128>, 4, 2, 1>(s, a, st);
   if (s.dtype == 0 && s.hd == 64) return run<float, 64, SimtTile<64>, 4, 2, 2>(s, a, st);
   return cudaErrorInvalidValue;
