@@ -68,12 +68,28 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+// x = upper part + rest: the upper 16 bits of x (x rounded to bf16 towards zero) and
+// what is left, rounded to nearest. Together they carry x to 2^-16. The rest has
+// x's sign and is never zero beside an x that is not: an infinite key or value
+// times both parts then is the infinity that it is times x, where inf * 0 or inf - inf
+// would be a NaN. (The smallest normal number in its place adds nothing otherwise.)
+__device__ __forceinline__ uint32_t upper2(float x, float y) {
+  return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-// x - bf16(x): exact in fp32, so bf16(x) + bf16(x - bf16(x)) carries 16 bits of x.
-__device__ __forceinline__ float rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float rest(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+constexpr float TINY = 1.17549435e-38f;  // 2^-126
+__device__ __forceinline__ uint32_t rest2_weights(float x, float y) {  // x, y >= 0
+  return pack2(fmaxf(rest(x), TINY), fmaxf(rest(y), TINY));
+}
+__device__ __forceinline__ float rest_signed(float x) {
+  const float r = rest(x);
+  return r == 0.f && x != 0.f ? copysignf(TINY, x) : r;
+}
+__device__ __forceinline__ uint32_t rest2(float x, float y) { return pack2(rest_signed(x), rest_signed(y)); }
 
 // A running reference may lie this far (log2 units) below the maximum before it
 // moves: weights stay below 2^8, and the rescaling of o becomes rare.
@@ -143,13 +159,13 @@ struct MmaTile {
           const float x0 = (a.x * w.x - b.x * w.y) * scale, x1 = (a.y * w.z - b.y * w.w) * scale;
           const float y0 = (a.x * w.y + b.x * w.x) * scale, y1 = (a.y * w.w + b.y * w.z) * scale;
           if (ONE) {
-            q[k][n][e] = lower ? pack2(rest(x0), rest(x1)) : pack2(x0, x1);
-            q[k + KS / 2][n][e] = lower ? pack2(rest(y0), rest(y1)) : pack2(y0, y1);
+            q[k][n][e] = lower ? rest2(x0, x1) : upper2(x0, x1);
+            q[k + KS / 2][n][e] = lower ? rest2(y0, y1) : upper2(y0, y1);
           } else {
-            q[k][n][e] = pack2(x0, x1);
-            q[k + KS / 2][n][e] = pack2(y0, y1);
-            q[k][NT - NH + n][e] = pack2(rest(x0), rest(x1));
-            q[k + KS / 2][NT - NH + n][e] = pack2(rest(y0), rest(y1));
+            q[k][n][e] = upper2(x0, x1);
+            q[k + KS / 2][n][e] = upper2(y0, y1);
+            q[k][NT - NH + n][e] = rest2(x0, x1);
+            q[k + KS / 2][NT - NH + n][e] = rest2(y0, y1);
           }
         }
       }
@@ -240,10 +256,10 @@ struct MmaTile {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (ONE) {
-          ph[n][e] = transpose8x8(lower ? pack2(rest(w[2 * e]), rest(w[2 * e + 1])) : pack2(w[2 * e], w[2 * e + 1]));
+          ph[n][e] = transpose8x8(lower ? rest2_weights(w[2 * e], w[2 * e + 1]) : upper2(w[2 * e], w[2 * e + 1]));
         } else {
-          ph[n][e] = transpose8x8(pack2(w[2 * e], w[2 * e + 1]));
-          pl[n][e] = transpose8x8(pack2(rest(w[2 * e]), rest(w[2 * e + 1])));
+          ph[n][e] = transpose8x8(upper2(w[2 * e], w[2 * e + 1]));
+          pl[n][e] = transpose8x8(rest2_weights(w[2 * e], w[2 * e + 1]));
         }
       }
     }

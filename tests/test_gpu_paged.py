@@ -400,6 +400,71 @@ def test_decode_lengths_split_and_joined(dtype, pos):
     run_checked(Step(len(pos), pos, 4, 2, 128, 64, dtype=dtype))
 
 
+def test_decode_many_short_and_one_long_sequence():
+    """More sequences than a block has threads (several to a thread in the plan, several rounds of the join), some not
+    running, and a long one among them whose parts a whole block joins."""
+    r = np.random.Generator(np.random.Philox(77))
+    pos = r.integers(-1, 40, 700)
+    pos[300] = 30000
+    run_checked(Step(77, list(pos), 6, 2, 64, 32))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_long_sequences_of_many_heads(dtype):
+    """Units of many parts and more heads than the join has blocks."""
+    run_checked(Step(78, [4000, 3900, 100], 256, 16, 64, 64, dtype=dtype))
+
+
+def test_decode_nothing_running():
+    """No sequence runs: zeros, nothing written."""
+    run_checked(Step(79, [-1] * 5, 4, 2, 128, 16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,H_kv", [(4, 2), (12, 2), (32, 2)])
+def test_decode_masked_garbage_and_infinities(dtype, H, H_kv):
+    """Infinite and NaN entries outside the attended positions (before the window, behind the last position, other heads'
+    and other sequences' rows) change nothing; infinite attended values and keys come through as the formula has it:
+    a value times a positive weight is infinite, a key with a score of minus infinity has no weight."""
+    s = Step(80, [333, 40], H, H_kv, 128, 16, window=100, dtype=dtype)
+    G = H // H_kv
+    first = s.run().clone()
+    torch.cuda.synchronize()
+    lo = 333 - 100 + 1
+    page = int(s.table_h[0, lo // 16])
+    for bad in (float("inf"), float("-inf"), float("nan"), torch.finfo(TD[dtype]).min):
+        s.kp[page, :, : lo % 16] = bad
+        s.vp[page, :, : lo % 16] = bad
+        last = int(s.table_h[0, 333 // 16])
+        s.kp[last, :, 333 % 16 + 1:] = bad
+        s.vp[last, :, 333 % 16 + 1:] = bad
+        assert torch.equal(s.run(), first), bad
+    j = 300
+    row = int(s.table_h[0, j // 16]), 0, j % 16
+    kept = s.vp[row].clone()
+    s.vp[row][5] = float("inf")
+    s.vp[row][6] = float("-inf")
+    out = s.run()
+    torch.cuda.synchronize()
+    assert (out[0, :G, 5] == float("inf")).all() and (out[0, :G, 6] == float("-inf")).all()
+    keep = torch.arange(128, device="cuda") % 128
+    keep = (keep != 5) & (keep != 6)
+    assert torch.equal(out[0, :G][:, keep], first[0, :G][:, keep])
+    assert torch.equal(out[0, G:], first[0, G:]) and torch.equal(out[1], first[1])
+    # a key against which every query of its group scores minus infinity is as good as absent
+    s.vp[row].copy_(kept)
+    q = oracle.rope(host(s.q)[:1], np.full((1, H), 333), 10000.0)[0]
+    c = int(np.argmax(np.abs(q[:G]).min(0)))
+    for h in range(G):
+        s.q[0, h] = s.q[0, 0]  # one sign for the group
+    s.kp[row][c] = float("-inf") if q[0, c] > 0 else float("inf")
+    without = s.run().clone()
+    s.vp[row].fill_(0)
+    torch.cuda.synchronize()
+    assert torch.isfinite(without).all()
+    assert torch.equal(s.run(), without)
+
+
 def test_decode_far_positions_and_large_scores():
     """Angles at positions near 2^24 (fp32 cannot hold them), and scores of some hundreds: the running maximum has
     to move, and most weights underflow."""
@@ -473,8 +538,8 @@ def test_decode_pages_outside_the_pool(dtype):
 
 
 def test_decode_repeats_bit_for_bit_on_any_stream_and_in_a_graph():
-    """Twenty repeats on two streams and replays of a graph all give the first result's bits: the order of the joined
-    parts is fixed, and the workspace's counters are zero again after each."""
+    """Twenty repeats on two streams and replays of a graph all give the first result's bits: the parts are joined in
+    the order of the keys."""
     s = Step(21, [5000, 17, 0, 333, -1, 2048], 8, 4, 128, 16, inject=True)
     first = s.run().clone()
     torch.cuda.synchronize()
@@ -503,12 +568,13 @@ def test_decode_repeats_bit_for_bit_on_any_stream_and_in_a_graph():
 
 
 def test_workspace_may_serve_layers_of_other_shapes():
-    """One workspace, sized for the largest, for layers of different head counts and types in turn."""
+    """One workspace, sized for the largest and with any content, for layers of different head counts and types in
+    turn."""
     steps = [Step(1, [700, 5], 8, 8, 128, 16), Step(2, [9000], 4, 1, 64, 32), Step(3, [64, 65, 2], 6, 2, 128, 16, dtype="f32")]
     ws = max((s.ws for s in steps), key=torch.numel)
     for _ in range(2):
         for s in steps:
-            s.ws = ws
+            s.ws = ws.fill_(0xff)
             run_checked(s)
 
 
@@ -597,3 +663,49 @@ def test_serving_run(dtype, H, H_kv, window, inject):
                 within(out[b], ref, tol, f"step {it} layer {l} sequence {b}")
         lens = lens2
     assert refused < 14 * B
+
+
+def test_step_captured_in_a_graph_runs_on():
+    """A whole serving step (tables in place, two layers) in one graph: replays continue the sequences by a token each,
+    as separate calls do."""
+    def build():
+        T = PageTables(3, 16, 8, 20, 64)
+        L = [PagedLayerState(T, 4, 64, 2) for _ in range(2)]
+        for x in L:
+            x.k_pages.zero_()
+            x.v_pages.zero_()
+        return T, L
+
+    gen = generator(91)
+    q, k, v = normal(gen, (3, 4, 64), "bf16"), normal(gen, (3, 2, 64), "bf16"), normal(gen, (3, 2, 64), "bf16")
+    new = torch.tensor([1, 0, 1], device="cuda")
+    results = []
+    for captured in (False, True):
+        T, L = build()
+        T.step(torch.tensor([20, 5, 0], device="cuda"), 64)
+        for x in L:
+            x.write(T.slots, T.pos, k.repeat(22, 1, 1)[:64], v.repeat(22, 1, 1)[:64])
+
+        def step():
+            pos, _ = T.step(new, 3, 1)
+            for x in L:
+                x.step(pos, q, k, v)
+
+        if captured:
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step()
+            for _ in range(30):
+                g.replay()
+        else:
+            for _ in range(30):
+                step()
+        torch.cuda.synchronize()
+        assert T.lengths.tolist() == [50, 5, 30] and int(T.n_free) == 20 - 4 - 1 - 2
+        results.append([x.out.clone() for x in L] + [T.block_table.clone(), L[1].k_pages.clone()])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert mg.maglev_device_status() == 0
+    with pytest.raises(ValueError):
+        T.step(new, 65)
