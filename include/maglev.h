@@ -96,8 +96,9 @@ typedef struct {
  * heads (H % H_kv == 0; query head h reads head h / (H / H_kv)), hd 64 or 128,
  * page_size a power of two in [16, 256], window W >= 1 (keys max(0, p-W+1)..p) or
  * 0 (every position up to p), the other fields as in maglev_decode_desc. Gate
- * logits are [4, H_kv] ([2, H_kv] with shared_kv_gates). page numbers, slots
- * and lengths come from the device: one that lies outside the pool or the
+ * logits are [4, H_kv] ([2, H_kv] with shared_kv_gates). Page numbers, slots
+ * and lengths come from the device (arrays of them need their type's alignment
+ * only): one that lies outside the pool or the
  * table is never followed, and the call records MAGLEV_ERR_BOUNDS in the device
  * status word (in every build). */
 typedef struct {

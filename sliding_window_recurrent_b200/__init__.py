@@ -113,7 +113,9 @@ class _Lazy:
                 fn.argtypes = args
                 fn.restype = res
             self._dll = dll
-        return getattr(self._dll, name)
+        fn = getattr(self._dll, name)
+        setattr(self, name, fn)  # later lookups do not come here
+        return fn
 
 
 _lib = _Lazy()

@@ -95,6 +95,15 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
       return fail(MAGLEV_ERR_INVALID_ARG, "%s must be 16-byte aligned", #p);              \
   } while (0)
 
+// Index arrays (lengths, positions, slots, page numbers) are read one by one: their
+// type's alignment is enough, so that slices of a caller's arrays can be passed.
+#define NEED_INDEX(p)                                                                      \
+  do {                                                                                    \
+    if ((p) == nullptr) return fail(MAGLEV_ERR_INVALID_ARG, "%s must not be NULL", #p);   \
+    if (reinterpret_cast<uintptr_t>(p) % sizeof(*(p)) != 0)                               \
+      return fail(MAGLEV_ERR_INVALID_ARG, "%s must be %d-byte aligned", #p, (int)sizeof(*(p))); \
+  } while (0)
+
 size_t elt(int dtype) { return dtype == MAGLEV_BF16 ? 2 : 4; }
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -1006,17 +1015,17 @@ maglev_status maglev_page_tables(const maglev_paged_desc* d, const int64_t* ctx_
   if (pad > 0 && (n_tokens % pad != 0 || n_tokens / pad != d->B))
     return fail(MAGLEV_ERR_INVALID_ARG, "n_tokens must be B * pad when pad > 0");
   if (d->B == 0) return MAGLEV_OK;
-  NEED_PTR(ctx_len);
-  NEED_PTR(new_len);
-  NEED_PTR(free_pages);
-  NEED_PTR(n_free);
-  NEED_PTR(block_table);
-  NEED_PTR(seq_len);
-  NEED_PTR(n_free_out);
-  NEED_PTR(cu_tokens);
+  NEED_INDEX(ctx_len);
+  NEED_INDEX(new_len);
+  NEED_INDEX(free_pages);
+  NEED_INDEX(n_free);
+  NEED_INDEX(block_table);
+  NEED_INDEX(seq_len);
+  NEED_INDEX(n_free_out);
+  NEED_INDEX(cu_tokens);
   if (n_tokens > 0) {
-    NEED_PTR(pos);
-    NEED_PTR(slots);
+    NEED_INDEX(pos);
+    NEED_INDEX(slots);
   }
   NEED_PTR(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1038,8 +1047,8 @@ maglev_status maglev_paged_write(const maglev_paged_desc* d, int64_t n, const in
   if (n > (int64_t)1 << 31) return fail(MAGLEV_ERR_UNSUPPORTED, "n must be at most 2^31");
   if (d->inject && !pos) return fail(MAGLEV_ERR_INVALID_ARG, "entries stored as they are (pos NULL) take no injection");
   if (n == 0) return MAGLEV_OK;
-  NEED_PTR(slots);
-  OPT_PTR(pos);
+  NEED_INDEX(slots);
+  if (pos) NEED_INDEX(pos);
   NEED_PTR(k);
   NEED_PTR(v);
   NEED_PTR(k_pages);
@@ -1071,11 +1080,11 @@ maglev_status maglev_paged_decode_step(const maglev_paged_desc* d, const int64_t
   maglev_status st = check_paged(d);
   if (st != MAGLEV_OK) return st;
   if (d->B == 0) return MAGLEV_OK;
-  NEED_PTR(pos);
+  NEED_INDEX(pos);
   NEED_PTR(q);
   NEED_PTR(k);
   NEED_PTR(v);
-  NEED_PTR(block_table);
+  NEED_INDEX(block_table);
   NEED_PTR(k_pages);
   NEED_PTR(v_pages);
   NEED_PTR(out);

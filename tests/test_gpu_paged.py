@@ -162,6 +162,32 @@ def test_page_tables_many_returned_pages():
         t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table))
 
 
+def test_index_arrays_may_be_slices():
+    """Lengths, positions, slots and tables at odd places of larger arrays (their type's alignment only)."""
+    B, ps, columns = 5, 16, 3
+    lens, new, n_tokens, free, table, pool = draw_tables(3, B, ps, columns, 0, True, 1.0)
+    t = Tables(lens, new, n_tokens, 0, ps, free, table, pool)
+
+    def odd(x):
+        big = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")
+        big[1:] = x.flatten()
+        return big[1:].view(x.shape)
+
+    for name in ("lens", "new", "free", "n_free", "table", "seq_len", "n_out", "cu", "pos", "slots"):
+        setattr(t, name, odd(getattr(t, name)))
+    t.run()
+    t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table))
+    s = Step(3, [40, 3, -1], 4, 2, 64, 16)
+    s.pos, s.table = odd(s.pos), odd(s.table)
+    run_checked(s)
+    k = normal(generator(3), (3, 2, 64), "bf16")
+    kp, vp = torch.zeros(2, 2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    mg.maglev_paged_write(desc(hd=64, num_pages=2), 3, odd(torch.tensor([3, 31, 16], device="cuda")),
+                          odd(torch.tensor([0, 0, 0], device="cuda")), k, k, None, None, None, kp, vp)
+    torch.cuda.synchronize()
+    assert torch.equal(vp[1, :, 15], k[1]) and torch.equal(kp[1, :, 0], k[2])
+
+
 def test_page_tables_bad_lengths_and_pages():
     """Lengths outside a row are refused; a page number outside the pool gives no slot and is recorded; a free count
     above the pool's size is cut and recorded. (All are bounds checks of the kernel; nothing is followed.)"""

@@ -190,17 +190,21 @@ def test_write_and_step_refuse_bad_layers(call, bad, status, text):
 
 
 def test_pointers_are_checked():
-    for name in ("ctx_len", "new_len", "free_pages", "n_free", "block_table", "seq_len", "n_free_out", "cu_tokens", "pos",
-                 "slots", "workspace"):
+    """NULL and misaligned pointers are refused by name: 16 bytes for data, the type's size for index arrays."""
+    for name, size in (("ctx_len", 8), ("new_len", 8), ("free_pages", 4), ("n_free", 4), ("block_table", 4),
+                       ("seq_len", 8), ("n_free_out", 4), ("cu_tokens", 8), ("pos", 8), ("slots", 8), ("workspace", 16)):
         refused(tables, INV, name, desc(), **{name: None})
-        refused(tables, INV, "aligned", desc(), **{name: FAKE + 8})
-    for name in ("slots", "k", "v", "k_pages", "v_pages"):
-        refused(write, INV, name, desc(), **{name: None})
-        refused(write, INV, "aligned", desc(), **{name: FAKE + 4})
-    refused(write, INV, "aligned", desc(), pos=FAKE + 8)
-    for name in ("pos", "q", "k", "v", "block_table", "k_pages", "v_pages", "out"):
+        refused(tables, INV, f"{name} must be {size}-byte aligned", desc(), **{name: FAKE + size // 2})
+        if size < 16:  # the type's alignment will do: the next refusal is another one
+            refused(tables, INV, "workspace", desc(), **{name: FAKE + size, "workspace": None})
+    for name, size in (("slots", 8), ("pos", 8), ("k", 16), ("v", 16), ("k_pages", 16), ("v_pages", 16)):
+        if name != "pos":
+            refused(write, INV, name, desc(), **{name: None})
+        refused(write, INV, f"{name} must be {size}-byte aligned", desc(), **{name: FAKE + size // 2})
+    for name, size in (("pos", 8), ("q", 16), ("k", 16), ("v", 16), ("block_table", 4), ("k_pages", 16), ("v_pages", 16),
+                       ("out", 16), ("workspace", 16)):
         refused(step, INV, name, desc(), **{name: None})
-        refused(step, INV, "aligned", desc(), **{name: FAKE + 4})
+        refused(step, INV, f"{name} must be {size}-byte aligned", desc(), **{name: FAKE + size // 2})
     for name, arg in (("R_k", "R_k"), ("R_v", "R_v"), ("gate_logits", "gates")):
         refused(write, INV, name, desc(inject=1), **{arg: None})
     for name, arg in (("krec_rot", "krec"), ("vrec", "vrec"), ("gate_logits", "gates")):
