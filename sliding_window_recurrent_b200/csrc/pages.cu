@@ -395,8 +395,11 @@ __global__ void __launch_bounds__(WRITE_THREADS, sizeof(T) == 2 ? 3 : 2) paged_w
     gvr = gate_value(gates[(s.vg + 1) * s.Hkv + h]);
   }
   if (MODE != WRITE_COPY) {
-    for (int i = threadIdx.x; i < ntok * HALF; i += WRITE_THREADS)
-      turn[i] = rope_turn(pos[t0 + i / HALF], rf.turns[i % HALF]);
+    // pairs 8u + e of a token at [e / 2][u][e % 2]: the lanes of a row read side by side
+    for (int i = threadIdx.x; i < ntok * HALF; i += WRITE_THREADS) {
+      const int c = i % HALF, e = c % 8;
+      turn[i - c + (e / 2 * TPR + c / 8) * 2 + e % 2] = rope_turn(pos[t0 + i / HALF], rf.turns[c]);
+    }
     __syncthreads();
   }
   for (int tt = row / heads; tt - row / heads < ntok; tt += pass) {  // whole blocks: the RMS sums shuffle
@@ -420,10 +423,10 @@ __global__ void __launch_bounds__(WRITE_THREADS, sizeof(T) == 2 ? 3 : 2) paged_w
       } else {
         load8f(reinterpret_cast<const T*>(&k1), x1);
         load8f(reinterpret_cast<const T*>(&k2), x2);
-        const float4* tw = reinterpret_cast<const float4*>(turn + tt * HALF + 8 * u);
+        const float4* tw = reinterpret_cast<const float4*>(turn + tt * HALF) + u;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          const float4 w = tw[e / 2];  // two pairs' angles
+          const float4 w = tw[e / 2 * TPR];  // two pairs' angles
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float cs = i ? w.z : w.x, sn = i ? w.w : w.y;
