@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
   T* vp = static_cast<T*>(a.vp);
   T* out = static_cast<T*>(a.out);
 
-  asm volatile("griddepcontrol.launch_dependents;");  // the join's blocks may take the places that come free
+  wait_for_last();
+  let_next_start();  // the join's blocks may take the places that come free
   const Steps steps = form_plan(plan, s, a);
   const int64_t per = steps.per, total = steps.total;
   const int me = blockIdx.x * NW + warp;
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedSha
       p.first = p.rest + (base > steps.per * w0 ? stride / 2 : 0);  // behind other units of warp w0's range
       if (p.np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
     }
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written
+    if (!waited) wait_for_last();  // the parts are written
     waited = true;
     // (the barrier also ends the last round's use of the shared rows)
     const int help = __syncthreads_or(p.np > ALONE) ? per_block : 0;
@@ -998,15 +999,14 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   if (grid > most) grid = most;
   a.warps = (int)grid * NW;
   a.inv_warps = 1.0 / a.warps;
-  kern<<<(unsigned)grid, NW * 32, smem, st>>>(s, a, rope_freqs(HD, s.log2_base));
-  e = cudaGetLastError();
+  e = launch_dependent(kern, dim3((unsigned)grid), NW * 32, smem, st, s, a, rope_freqs(HD, s.log2_base));
   if (e != cudaSuccess) return e;
   // the join: scheduled as the first kernel ends, its blocks wait for that before they read a part
   const int64_t heads = (int64_t)s.B * s.H, blocks = 2 * num_sms();
   int per_block = (int)((heads + blocks - 1) / blocks < JOIN_WARPS ? (heads + blocks - 1) / blocks : JOIN_WARPS);
   const int64_t need = (heads + per_block - 1) / per_block;
-  return launch_dependent(paged_join_kernel<T, HD>, (unsigned)(need < blocks ? need : blocks), JOIN_WARPS * 32, st, s, a,
-                          per_block);
+  return launch_dependent(paged_join_kernel<T, HD>, dim3((unsigned)(need < blocks ? need : blocks)), JOIN_WARPS * 32, 0,
+                          st, s, a, per_block);
 }
 
 }  // namespace

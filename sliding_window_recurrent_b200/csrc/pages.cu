@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
                                                                  int* err) {
   __shared__ uint2 sums[4][32];
   __shared__ FillRequests requests;
-  asm volatile("griddepcontrol.launch_dependents;");
+  wait_for_last();
+  let_next_start();
   const PlanViews w = plan_views(ws, a.B);
   const int tid = threadIdx.x, chunk = PLAN_EACH * blockDim.x;
   const int cap = a.max_pages << shift;  // at most 2^30, like n_tokens
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
 __global__ void __launch_bounds__(FILL_ROWS) page_fill_kernel(PageTablesArgs a, void* ws, int shift, int* err) {
   __shared__ FillRequests requests;
   const PlanViews w = plan_views(ws, a.B);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+  wait_for_last();  // the plan is written
   const PlanTotals tot = *w.totals;
   const int2* fin = stage_finished(w, tot.finished, requests);
   fill_rows(a, w, tot, fin, shift, (int64_t)blockIdx.x * FILL_ROWS, requests, err);  // has a barrier before it reads fin
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(WRITE_THREADS, sizeof(T) == 2 ? 3 : 2) paged_w
   const int64_t t0 = (int64_t)blockIdx.x * tile;
   const int ntok = (int)(n - t0 < tile ? n - t0 : tile);
   const int64_t nslots = (int64_t)s.num_pages << shift;
+  wait_for_last();
   const int u = threadIdx.x % TPR, row = threadIdx.x / TPR, h = blockIdx.y * heads + row % heads;
   const bool mine = row < heads * pass && h < s.Hkv;
   float gkl = 1.f, gkr = 0.f, gvl = 1.f, gvr = 0.f;
@@ -478,13 +480,12 @@ cudaError_t write_pages(const PagedShape& s, int64_t n, const int64_t* slots, co
   const RopeFreqs& rf = rope_freqs(HD, s.log2_base);
   const int shift = log2_of(s.page_size);
   auto go = [&](auto kern) {
-    kern<<<blocks, WRITE_THREADS, 0, st>>>(s, rf, shift, n, tile, heads, pass, slots, pos, (const T*)k, (const T*)v,
-                                           (const T*)Rk, (const T*)Rv, gates, (T*)kp, (T*)vp, err);
+    return launch_dependent(kern, blocks, WRITE_THREADS, 0, st, s, rf, shift, n, tile, heads, pass, slots, pos,
+                            (const T*)k, (const T*)v, (const T*)Rk, (const T*)Rv, gates, (T*)kp, (T*)vp, err);
   };
-  if (!pos) go(paged_write_kernel<T, HD, WRITE_COPY>);
-  else if (!s.inject) go(paged_write_kernel<T, HD, WRITE_ROPE>);
-  else go(paged_write_kernel<T, HD, WRITE_MIX>);
-  return cudaGetLastError();
+  if (!pos) return go(paged_write_kernel<T, HD, WRITE_COPY>);
+  if (!s.inject) return go(paged_write_kernel<T, HD, WRITE_ROPE>);
+  return go(paged_write_kernel<T, HD, WRITE_MIX>);
 }
 
 // Token rows that the plan's block fills itself.
@@ -502,11 +503,10 @@ cudaError_t launch_page_tables(const PageTablesArgs& a, void* workspace, int* er
   int threads = (a.B + PLAN_EACH - 1) / PLAN_EACH;  // few requests: fewer warps to sum over
   if (one && a.n_tokens > threads) threads = (int)a.n_tokens;
   threads = threads < 64 ? 64 : threads > PLAN_THREADS ? PLAN_THREADS : (threads + 31) / 32 * 32;
-  page_plan_kernel<<<1, threads, 0, st>>>(a, workspace, shift, one, err);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_dependent(page_plan_kernel, dim3(1), threads, 0, st, a, workspace, shift, one, err);
   if (e != cudaSuccess || one) return e;
-  return launch_dependent(page_fill_kernel, (unsigned)((a.n_tokens + FILL_ROWS - 1) / FILL_ROWS), FILL_ROWS, st, a,
-                          workspace, shift, err);
+  return launch_dependent(page_fill_kernel, dim3((unsigned)((a.n_tokens + FILL_ROWS - 1) / FILL_ROWS)), FILL_ROWS, 0, st,
+                          a, workspace, shift, err);
 }
 
 cudaError_t launch_paged_write(const PagedShape& s, int64_t n, const int64_t* slots, const int64_t* pos, const void* k,

@@ -593,6 +593,49 @@ def test_decode_repeats_bit_for_bit_on_any_stream_and_in_a_graph():
     s.check(before)
 
 
+def test_calls_follow_their_producers_and_precede_their_consumers():
+    """The calls' blocks may be scheduled before the stream's last kernel has ended, but read and write nothing before:
+    inputs made by slow kernels just before, outputs read and inputs overwritten just behind, many times over."""
+    s = Step(31, [900, 5, 333, 64], 4, 2, 128, 16)
+    want = s.run().clone()
+    torch.cuda.synchronize()
+    slow = torch.randn(3000, 2999, device="cuda")
+    q, pos, table = s.q.clone(), s.pos.clone(), s.table.clone()
+    kept = []
+    for i in range(40):
+        zero = (slow @ slow.T)[:1, :1] * 0  # a kernel of some 100 us before each input is there
+        s.q.copy_(q + zero.to(q.dtype))
+        s.pos.copy_(pos + zero.to(pos.dtype).view(1))
+        s.table.copy_(table + zero.to(table.dtype))
+        kept.append(s.run().clone())
+        s.q.fill_(float("nan"))
+        s.pos.fill_(-1)
+        s.table.fill_(-1)
+        s.out.fill_(0)
+    torch.cuda.synchronize()
+    for i, o in enumerate(kept):
+        assert torch.equal(o, want), i
+    # tables, write and step one behind the other, on a stream that waits for another one's work
+    T = PageTables(2, 16, 8, 16, 64)
+    L = PagedLayerState(T, 2, 64)
+    k, q = normal(generator(5), (64, 2, 64), "bf16"), normal(generator(6), (2, 2, 64), "bf16")
+    side, outs = torch.cuda.Stream(), []
+    for i in range(20):
+        T.lengths.zero_()
+        T.n_free.fill_(16)
+        new = (slow @ slow.T)[:1, :2].to(torch.int64) * 0 + torch.tensor([33, 31], device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            pos, slots = T.step(new.view(2), 64)
+            L.write(slots, pos, k, k)
+            pos, _ = T.step(torch.ones_like(new.view(2)), 2, 1)
+            outs.append(L.step(pos, q, k[:2], k[:2]).clone())
+        torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.isfinite(outs[0]).all() and all(torch.equal(o, outs[0]) for o in outs)
+    assert mg.maglev_device_status() == 0
+
+
 def test_workspace_may_serve_layers_of_other_shapes():
     """One workspace, sized for the largest and with any content, for layers of different head counts and types in
     turn."""
