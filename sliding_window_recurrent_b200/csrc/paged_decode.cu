@@ -23,6 +23,20 @@
 // (m, l, o) of the at most two that do not in the workspace. A second kernel, whose
 // blocks are scheduled while the first one ends, joins the parts in the order of
 // the keys: the same bits whatever ran first, and no block waits for another.
+//
+// Measured (one B200, GPU time in a graph; share of the bytes' time at 6535 GB/s):
+//   64 sequences of 64..4096, 10 heads of 128, bf16          109.2 us  0.96
+//   8 of 8192..65536, 32 query heads on 4 of 128, bf16        98.8 us  0.94
+//   64 of 128..8192, window 512, 10 of 128, bf16              34.3 us  0.74
+//   2 of 15005, 30010, 8 on 4 heads of 64, fp32               24.4 us  0.58
+//   1 of 190, 10 of 128, bf16                                  7.5 us  (latency)
+// Beside the streaming each call pays about 3.5 us from the launch to the first data
+// (positions, page numbers and entries are three loads that depend on one another),
+// 2 us for the join, and what the slowest SM takes longer than the average (3 to 8 us).
+// With 16 and more query heads to a key/value head the 64 products of a step keep
+// the eight warps of an SM busy (0.71 at 16 heads of 128).
+// Eight warps with two 8 KB stages each (128 KB in flight on an SM) are what HBM
+// needs; with twelve the SMs' shares drift apart and the slowest ends 20% late.
 #include "paged.cuh"
 
 namespace maglev {
