@@ -491,8 +491,9 @@ cudaError_t write_pages(const PagedShape& s, int64_t n, const int64_t* slots, co
   return go(paged_write_kernel<T, HD, WRITE_MIX>);
 }
 
-// Token rows that the plan's block fills itself.
-constexpr int64_t ONE_LAUNCH_ROWS = 1024;
+// Token rows that the plan's block fills itself: 512 single tokens take it 4.8 us, 1024
+// packed rows 6.2 to 7.3 us against 4.5 to 5 with the second launch.
+constexpr int64_t ONE_LAUNCH_ROWS = 512;
 
 }  // namespace
 

@@ -162,6 +162,17 @@ def test_page_tables_many_returned_pages():
         t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table))
 
 
+def test_page_tables_without_token_rows():
+    """Only ends and idle requests: no rows, pos and slots NULL; requests with tokens find no room and stay."""
+    table = np.array([[4, 2], [3, -1], [0, -1]], dtype=np.int32)
+    t = Tables([20, 7, 16], [-1, 0, 3], 0, 0, 16, [1], table, 6)
+    t.pos = t.slots = None
+    t.run()
+    torch.cuda.synchronize()
+    assert t.seq_len.tolist() == [0, 7, 16] and t.cu.tolist() == [0, 0, 0, 0] and t.n_out.tolist() == [3]
+    assert t.free[:3].tolist() == [1, 4, 2] and mg.maglev_device_status() == 0
+
+
 def test_index_arrays_may_be_slices():
     """Lengths, positions, slots and tables at odd places of larger arrays (their type's alignment only)."""
     B, ps, columns = 5, 16, 3
@@ -227,7 +238,7 @@ def entry_bound(pos, k, v, R_k, R_v, gates, ref_k, ref_v, dtype, eps=1e-6):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hd,H_kv,ps,n", [(128, 10, 16, 1), (64, 1, 32, 5), (128, 3, 64, 333), (64, 7, 256, 1000),
-                                          (128, 2, 128, 5000), (64, 10, 16, 2369)])
+                                          (128, 2, 128, 5000), (64, 10, 16, 2369), (128, 40, 32, 70), (64, 130, 16, 9)])
 @pytest.mark.parametrize("mode", ["copy", "rope", "mix", "mix_shared"])
 def test_paged_write(dtype, hd, H_kv, ps, n, mode):
     """Entries against the oracle within the bounds, every other slot as it was (NaN bytes included), rows with a
@@ -439,6 +450,27 @@ def test_decode_many_short_and_one_long_sequence():
 def test_decode_long_sequences_of_many_heads(dtype):
     """Units of many parts and more heads than the join has blocks."""
     run_checked(Step(78, [4000, 3900, 100], 256, 16, 64, 64, dtype=dtype))
+
+
+def test_decode_shared_prefix_pages_and_layers_side_by_side():
+    """Two sequences whose first pages are the same ones, and two layers (each its own pages and workspace) at once on
+    two streams."""
+    s = Step(81, [200, 150], 4, 2, 64, 16)
+    s.table_h[1, :8] = s.table_h[0, :8]
+    s.table.copy_(torch.from_numpy(s.table_h))
+    run_checked(s)
+    steps = [Step(82, [3000, 70, 512], 4, 2, 128, 32), Step(83, [2500, 9], 8, 1, 128, 16)]
+    want = [x.run().clone() for x in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(25):
+        for x, st in zip(steps, streams):
+            x.out.zero_()
+            st.wait_stream(torch.cuda.current_stream())
+            x.run(st)
+        torch.cuda.synchronize()
+        for x, w in zip(steps, want):
+            assert torch.equal(x.out, w)
 
 
 def test_decode_nothing_running():
@@ -778,3 +810,31 @@ def test_step_captured_in_a_graph_runs_on():
     assert mg.maglev_device_status() == 0
     with pytest.raises(ValueError):
         T.step(new, 65)
+
+
+def test_owners_refuse_tensors_the_library_would_misread():
+    """The classes check what the library, which sees addresses, cannot: shapes, types, strides and the device."""
+    T = PageTables(2, 16, 4, 8, 32)
+    L = PagedLayerState(T, 4, 64, 2)
+    new = torch.ones(2, dtype=torch.int64, device="cuda")
+    for bad in (new.int(), new.cpu(), torch.ones(3, dtype=torch.int64, device="cuda"), torch.ones(4, dtype=torch.int64, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="new_len"):
+            T.step(bad, 2)
+    pos, slots = T.step(new, 2)
+    k = normal(generator(1), (2, 2, 64), "bf16")
+    with pytest.raises(ValueError, match="k must"):
+        L.write(slots, pos, k[:1], k)
+    with pytest.raises(ValueError, match="v must"):
+        L.write(slots, pos, k, k.float())
+    with pytest.raises(ValueError, match="pos must"):
+        L.write(slots, pos[:1], k, k)
+    q = normal(generator(1), (2, 4, 64), "bf16")
+    with pytest.raises(ValueError, match="q must"):
+        L.step(pos, q[:, :2], k, k)
+    with pytest.raises(ValueError, match="k must"):
+        L.step(pos, q, q[:, ::2], k)
+    J = PagedLayerState(T, 4, 64, 2, inject=True, d_mem=16)
+    with pytest.raises(ValueError, match="gates"):
+        J.step(pos, q, k, k)
+    with pytest.raises(ValueError, match="R_k"):
+        J.write(slots, pos, k, k, gates=torch.zeros(4, 2, device="cuda"))
