@@ -33,8 +33,11 @@
 // Beside the streaming each call pays about 3.5 us from the launch to the first data
 // (positions, page numbers and entries are three loads that depend on one another),
 // 2 us for the join, and what the slowest SM takes longer than the average (3 to 8 us).
-// With 16 and more query heads to a key/value head the 64 products of a step keep
-// the eight warps of an SM busy (0.71 at 16 heads of 128).
+// More than 8 (fp32: 4) query heads to a key/value head are shared by a team of two or
+// four warps, each with its own heads, over one ring of stages: the cache is read
+// once for up to 32 (16) heads. Their arithmetic then is what binds: 0.76 of the
+// bytes' time at 16 heads of 128, 0.43 at 24, 0.66 at 8 in fp32 (0.72, 0.42, 0.45 with
+// wider tiles or several passes).
 // Eight warps with two 8 KB stages each (128 KB in flight on an SM) are what HBM
 // needs; with twelve the SMs' shares drift apart and the slowest ends 20% late.
 #include "paged.cuh"
@@ -489,9 +492,9 @@ struct DecodeArgs {
   const float* gates;
   const int32_t* table;
   void *kp, *vp, *out;
-  float* parts;      // [warps][2][heads][PART_ROW]
-  int warps;         // of the grid
-  double inv_warps;
+  float* parts;      // [teams][2][heads][PART_ROW]
+  int teams;         // of the grid
+  double inv_teams;
   int shift;         // log2 of the page size
   int heads, units;  // query heads of a unit (the last may have fewer), units of a sequence
   float scale_log2;
@@ -528,19 +531,19 @@ __device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeAr
 // The costs of all units in order make one line, which is cut into equal ranges.
 // It follows from the positions alone: every block of both kernels forms the same
 // sums. Thread i covers `chunk` sequences from i * chunk.
-template <int THREADS>
+template <int THREADS, int TEAMS>
 struct Plan {
   int64_t before[THREADS];  // costs (of one unit each) of the sequences before thread i's
   int64_t sums[THREADS / 32];
-  int owner[THREADS / 32];  // the thread whose sequences hold where the block's warp w begins
+  int owner[TEAMS];  // the thread whose sequences hold where the block's team i begins
 };
 // What a thread keeps of it.
 struct Steps {
-  int64_t total, per;  // cost of all units, of a warp's range
+  int64_t total, per;  // cost of all units, of a team's range
   int chunk;
 };
-template <int THREADS>
-__device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape& s, const DecodeArgs& a) {
+template <int THREADS, int TEAMS>
+__device__ __forceinline__ Steps form_plan(Plan<THREADS, TEAMS>& plan, const PagedShape& s, const DecodeArgs& a) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   Steps r;
   r.chunk = (s.B + THREADS - 1) / THREADS;
@@ -570,16 +573,16 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS>& plan, const PagedShape
   }
   plan.before[tid] = at;
   r.total *= a.units;
-  // total / warps, rounded up (a 64-bit division would take 0.3 us here)
-  r.per = r.total > 0 ? (int64_t)((double)(r.total - 1) * a.inv_warps) + 1 : 1;
-  if (r.per * a.warps < r.total) ++r.per;
+  // total / teams, rounded up (a 64-bit division would take 0.3 us here)
+  r.per = r.total > 0 ? (int64_t)((double)(r.total - 1) * a.inv_teams) + 1 : 1;
+  if (r.per * a.teams < r.total) ++r.per;
   if (r.per < MIN_COST) r.per = MIN_COST;
   at *= a.units;
   mine *= a.units;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int64_t t = r.per * ((int64_t)blockIdx.x * (THREADS / 32) + w) - at;
-    if (t >= 0 && t < mine) plan.owner[w] = tid;
+  for (int i = 0; i < TEAMS; ++i) {
+    const int64_t t = r.per * ((int64_t)blockIdx.x * TEAMS + i) - at;
+    if (t >= 0 && t < mine) plan.owner[i] = tid;
   }
   __syncthreads();
   return r;
@@ -592,8 +595,8 @@ struct Cursor {
   int64_t base;
 };
 // The one of place t, which thread `owner`'s sequences hold.
-template <int THREADS>
-__device__ __forceinline__ Cursor locate(const Plan<THREADS>& plan, const Steps& steps, const PagedShape& s,
+template <typename P>
+__device__ __forceinline__ Cursor locate(const P& plan, const Steps& steps, const PagedShape& s,
                                          const DecodeArgs& a, int owner, int64_t t) {
   Cursor c;
   c.b = owner * steps.chunk;
@@ -619,20 +622,26 @@ __device__ __forceinline__ void next_unit(Cursor& c, const PagedShape& s, const 
   while (c.q.cost == 0);
 }
 
-template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
+// TW warps form a team that shares its steps' stages and takes Tile::HEADS heads each.
+template <typename T, int HD, typename Tile, int TW, int NW, int STAGES, int OCC>
 __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s, DecodeArgs a,
                                                                   const __grid_constant__ RopeFreqs rf) {
   constexpr int HALF = HD / 2, NP = HALF / 32;
   constexpr int CPR = HD * (int)sizeof(T) / 16;    // 16-byte pieces of an entry
   constexpr int KV = KSTEP * HD * (int)sizeof(T);  // K (or V) bytes of a step
+  constexpr int TEAMS = NW / TW;
   extern __shared__ __align__(128) char sm[];
-  __shared__ Plan<NW * 32> plan;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  char* stages = sm + warp * STAGES * 2 * KV;
-  char* after = sm + NW * STAGES * 2 * KV;
+  __shared__ Plan<NW * 32, TEAMS> plan;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, team = warp / TW, rank = warp % TW;
+  char* stages = sm + team * STAGES * 2 * KV;
+  char* after = sm + TEAMS * STAGES * 2 * KV;
   char* room = after + warp * Tile::WARP_BYTES;
-  T* entry = reinterpret_cast<T*>(after + NW * Tile::WARP_BYTES) + warp * 2 * HD;  // the warp's new K, V
+  T* entry = reinterpret_cast<T*>(after + NW * Tile::WARP_BYTES) + warp * 2 * HD;  // the new K, V
   float2* turn = reinterpret_cast<float2*>(after + NW * (Tile::WARP_BYTES + 2 * HD * sizeof(T))) + warp * HALF;
+  auto team_sync = [&]() {
+    if (TW == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(TW * 32) : "memory");
+  };
   T* kp = static_cast<T*>(a.kp);
   T* vp = static_cast<T*>(a.vp);
   T* out = static_cast<T*>(a.out);
@@ -641,15 +650,15 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
   let_next_start();  // the join's blocks may take the places that come free
   const Steps steps = form_plan(plan, s, a);
   const int64_t per = steps.per, total = steps.total;
-  const int me = blockIdx.x * NW + warp;
-  const int64_t t0 = per * me, t1 = t0 + per < total ? t0 + per : total;  // the warp's range
+  const int me = blockIdx.x * TEAMS + team;
+  const int64_t t0 = per * me, t1 = t0 + per < total ? t0 + per : total;  // the team's range
   if (t0 >= t1) return;
   const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;  // units, query heads of a key/value head
-  Cursor cur = locate(plan, steps, s, a, plan.owner[warp], t0);  // the unit being worked on
+  Cursor cur = locate(plan, steps, s, a, plan.owner[team], t0);  // the unit being worked on
   // [begin, end) of a unit's steps lie in the range
   auto begin_of = [&](const Cursor& c) { return c.base + UNIT_COST > t0 ? c.base + UNIT_COST : t0; };
   auto end_of = [&](const Cursor& c) { return c.base + c.q.cost < t1 ? c.base + c.q.cost : t1; };
-  if (begin_of(cur) >= t1) return;  // the last unit's steps are the next warp's
+  if (begin_of(cur) >= t1) return;  // the last unit's steps are the next team's
 
   // ---- copies
   Cursor ahead = cur;
@@ -667,13 +676,13 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
   enter();
   page = arow[akey >> a.shift];
   const uint32_t stage0 = smem_u32(stages);
-  // a lane's i-th piece of a step's K or V lies 512 i bytes on, and goes to 512 i + put[i % PUTS]
-  constexpr int PUTS = CPR / 4;
+  // a lane's i-th piece of a step's K or V lies HOP i bytes on, and goes to HOP i + put[i % PUTS]
+  constexpr int HOP = 512 * TW, PERIOD = CPR / 4, PUTS = PERIOD > TW ? PERIOD / TW : 1, PIECES = KSTEP * CPR / 32 / TW;
   uint32_t put[PUTS];
 #pragma unroll
   for (int i = 0; i < PUTS; ++i) {
-    const int x = i * 32 + lane;
-    put[i] = piece<T, HD>(x / CPR, x % CPR) - 512 * i;
+    const int x = (i * TW + rank) * 32 + lane;
+    put[i] = piece<T, HD>(x / CPR, x % CPR) - HOP * i;
   }
   auto issue = [&](int st) {
     if (aleft > 0) {
@@ -681,22 +690,22 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
       // keys [from, to) of the step lie in the cache; the new entry (position p) does not
       const int from = ok ? ahead.q.lo - akey : KSTEP, to = ok ? ahead.q.p - akey : 0;
       const int64_t e = ((((int64_t)(ok ? page : 0) * s.Hkv + ahk) << a.shift) + (akey & (s.page_size - 1))) * HD +
-                        lane * (16 / (int)sizeof(T));
+                        (rank * 32 + lane) * (16 / (int)sizeof(T));
       const char* gk = reinterpret_cast<const char*>(kp + e);
       const char* gv = reinterpret_cast<const char*>(vp + e);
       const uint32_t dk = stage0 + st * 2 * KV;
       if (from <= 0 && to >= KSTEP) {
 #pragma unroll
-        for (int i = 0; i < KSTEP * CPR / 32; ++i) {
-          copy16(dk + put[i % PUTS] + 512 * i, gk + 512 * i, 16);
-          copy16(dk + put[i % PUTS] + 512 * i + KV, gv + 512 * i, 16);
+        for (int i = 0; i < PIECES; ++i) {
+          copy16(dk + put[i % PUTS] + HOP * i, gk + HOP * i, 16);
+          copy16(dk + put[i % PUTS] + HOP * i + KV, gv + HOP * i, 16);
         }
       } else {
-        for (int i = 0; i < KSTEP * CPR / 32; ++i) {
-          const int x = i * 32 + lane, r = x / CPR;
+        for (int i = 0; i < PIECES; ++i) {
+          const int x = (i * TW + rank) * 32 + lane, r = x / CPR;
           const int bytes = r >= from && r < to ? 16 : 0;
-          copy16(dk + piece<T, HD>(r, x % CPR), gk + 512 * i, bytes);
-          copy16(dk + piece<T, HD>(r, x % CPR) + KV, gv + 512 * i, bytes);
+          copy16(dk + piece<T, HD>(r, x % CPR), gk + HOP * i, bytes);
+          copy16(dk + piece<T, HD>(r, x % CPR) + KV, gv + HOP * i, bytes);
         }
       }
       bad = ok ? bad & ~(1u << st) : bad | (1u << st);
@@ -730,14 +739,16 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     const int64_t t = begin_of(cur), end = end_of(cur);  // steps [t, end) of the unit
     const int hk = cur.hu / groups;
     const int h0 = hk * per_kv + (cur.hu % groups) * a.heads;
-    const int heads = min(a.heads, (hk + 1) * per_kv - h0);
+    const int first = h0 + rank * Tile::HEADS;  // the warp's heads (none: the unit has fewer)
+    const int unit_heads = min(a.heads, (hk + 1) * per_kv - h0);
+    const int heads = TW == 1 ? unit_heads : min(Tile::HEADS, unit_heads - rank * Tile::HEADS);
     const bool has_new = end == cur.base + cur.q.cost, whole = t == cur.base + UNIT_COST && has_new;
     // every load of the unit at once: the query rows, and the new entry's parts
     const int64_t row = ((int64_t)cur.b * s.Hkv + hk) * HD;
     float k1[NP], k2[NP], v1[NP], v2[NP], kr1[NP], kr2[NP], vr1[NP], vr2[NP], ga = 0.f, gb = 0.f, gc = 0.f, gd = 0.f;
     int pg = -1;
-    tile.load_q(static_cast<const T*>(a.q) + ((int64_t)cur.b * s.H + h0) * HD, heads);
-    if (has_new) {
+    tile.load_q(static_cast<const T*>(a.q) + ((int64_t)cur.b * s.H + first) * HD, heads);
+    if (has_new && rank == 0) {
       const T *k = static_cast<const T*>(a.k) + row, *v = static_cast<const T*>(a.v) + row;
       const T *kr = static_cast<const T*>(a.krec) + row, *vr = static_cast<const T*>(a.vrec) + row;
       if (cur.hu % groups == 0) pg = a.table[(int64_t)cur.b * s.max_pages + (cur.q.p >> a.shift)];
@@ -764,7 +775,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     }
     turn_to(cur);
     tile.begin(turn, a.scale_log2, room, heads);
-    if (has_new) {
+    if (has_new && rank == 0) {
       const bool store = pg >= 0 && pg < s.num_pages;  // a bad page is recorded where its step is copied
       const int64_t e = ((((int64_t)(store ? pg : 0) * s.Hkv + hk) << a.shift) + (cur.q.p & (s.page_size - 1))) * HD;
 #pragma unroll
@@ -799,33 +810,36 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     for (; key < key_end; key += KSTEP) {
       const uint32_t ks = stage0 + st * 2 * KV, vs = ks + KV;
       copy_wait<STAGES - 1>();
-      __syncwarp();
+      team_sync();  // the team's copies of the stage have landed
       const int from = cur.q.lo - key, to = cur.q.p - key;  // keys [from, to] take part
       const bool gone = bad >> st & 1;
       if (to < KSTEP) {  // the new entry goes where its page holds it
-        char* dst = stages + st * 2 * KV;
-        for (int c = lane; c < CPR; c += 32) {
-          *reinterpret_cast<uint4*>(dst + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(entry)[c];
-          *reinterpret_cast<uint4*>(dst + KV + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(entry + HD)[c];
+        if (rank == 0) {
+          char* dst = stages + st * 2 * KV;
+          for (int c = lane; c < CPR; c += 32) {
+            *reinterpret_cast<uint4*>(dst + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(entry)[c];
+            *reinterpret_cast<uint4*>(dst + KV + piece<T, HD>(to, c)) = reinterpret_cast<const uint4*>(entry + HD)[c];
+          }
         }
-        __syncwarp();
+        team_sync();
       }
-      tile.step(
-          ks, vs, from <= 0 && to >= KSTEP - 1 && !gone,
-          [&](int r) { return r == to || (!gone && r >= from && r < to); }, room, heads);
-      __syncwarp();  // every lane has read the stage
+      if (TW == 1 || heads > 0)
+        tile.step(
+            ks, vs, from <= 0 && to >= KSTEP - 1 && !gone,
+            [&](int r) { return r == to || (!gone && r >= from && r < to); }, room, heads);
+      team_sync();  // every lane has read the stage
       issue(st);
       st = st + 1 == STAGES ? 0 : st + 1;
     }
     tile.finish(heads);
     if (whole) {
-      T* d = out + ((int64_t)cur.b * s.H + h0) * HD;
+      T* d = out + ((int64_t)cur.b * s.H + first) * HD;
       tile.each_out(
           heads, [](float l) { return l == 0.f ? 0.f : 1.f / l; },
           [&](int j, int c, float x) { d[j * HD + c] = from_f<T>(x); });
     } else {
       // the unit that holds the range's first place, or the one that goes on behind its last
-      float* part = a.parts + ((int64_t)me * 2 + (cur.base + UNIT_COST <= t0 ? 0 : 1)) * a.heads * PART_ROW;
+      float* part = a.parts + (((int64_t)me * 2 + (cur.base + UNIT_COST <= t0 ? 0 : 1)) * a.heads + first - h0) * PART_ROW;
       tile.each_out(
           heads, [](float) { return 1.f; }, [&](int j, int c, float x) { part[j * PART_ROW + c] = x; });
       tile.each_head(heads, [&](int j, float m, float l) {
@@ -838,10 +852,10 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
 }
 
 // ---------------------------------------------------------------------------
-// The outputs of units in several warps' ranges, and zeros for sequences that are
-// not running. A warp takes a (sequence, query head); where the head has more parts
-// than a warp has in flight, its block's warps take it together. A lane owns four
-// channels: what counts is the latency of parts in L2.
+// The outputs of units in several teams' ranges, and zeros for sequences that are
+// not running. A block's warps are divided among its (sequence, query head)s; one with
+// very many parts they take together. A lane owns four channels: what counts is the
+// latency of parts in L2.
 // ---------------------------------------------------------------------------
 constexpr int JOIN_WARPS = 8;
 constexpr int FLY = 8;  // parts of a lane in flight
@@ -910,19 +924,20 @@ __device__ __forceinline__ Joined join_parts(const Parts& p, int64_t stride, int
 template <typename T, int HD>
 __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedShape s, DecodeArgs a, int per_block) {
   constexpr int NW = JOIN_WARPS, V = HD / 4, SHARE = 32 / V;  // lanes that share four channels (hd 64: 2)
-  constexpr int ALONE = FLY * SHARE;                          // parts that a warp takes alone
-  __shared__ Plan<NW * 32> plan;
+  __shared__ Plan<NW * 32, 0> plan;
   __shared__ Parts parts[NW];
   __shared__ float4 so[NW][V];
   __shared__ float sm[NW], sl[NW];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % V * 4;
+  const int each = NW / per_block, rank = warp % each;  // warps of a head
+  const int longest = 4 * FLY * SHARE * each;                               // parts they take alone: four loads' time
   const Steps steps = form_plan(plan, s, a);  // reads nothing that the first kernel writes
-  const int64_t heads = (int64_t)s.B * s.H, stride = (int64_t)2 * a.heads * PART_ROW;  // from warp to warp
+  const int64_t heads = (int64_t)s.B * s.H, stride = (int64_t)2 * a.heads * PART_ROW;  // from team to team
   const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
   bool waited = false;
   for (int64_t at = (int64_t)blockIdx.x * per_block; at < heads; at += (int64_t)gridDim.x * per_block) {
-    const int64_t head = at + warp;
-    const bool mine = warp < per_block && head < heads;
+    const int64_t head = at + warp / each;
+    const bool mine = head < heads;
     Parts p{nullptr, nullptr, 1};
     if (mine) {
       const int b = (int)(head / s.H), h = (int)(head % s.H), hk = h / per_kv, in_kv = h - hk * per_kv;
@@ -930,35 +945,39 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedSha
       const int i = b / steps.chunk;
       int64_t base = plan.before[i];
       for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
-      // the unit's first step, and the warps that have steps of it
+      // the unit's first step, and the teams that have steps of it
       base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;
       const int w0 = (int)(base / steps.per);
       p.np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / steps.per) - w0 + 1 : 0;
       p.rest = a.parts + w0 * stride + in_kv % a.heads * PART_ROW;
-      p.first = p.rest + (base > steps.per * w0 ? stride / 2 : 0);  // behind other units of warp w0's range
-      if (p.np == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
+      p.first = p.rest + (base > steps.per * w0 ? stride / 2 : 0);  // behind other units of team w0's range
+      if (p.np == 0 && rank == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
     }
     if (!waited) wait_for_last();  // the parts are written
     waited = true;
     // (the barrier also ends the last round's use of the shared rows)
-    const int help = __syncthreads_or(p.np > ALONE) ? per_block : 0;
+    const int help = __syncthreads_or(p.np > longest) ? per_block : 0;
     if (help) {
-      if (lane == 0) parts[warp] = p;
+      if (rank == 0 && lane == 0) parts[warp / each] = p;
       __syncthreads();
     }
     Joined r{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
 #pragma unroll 1
-    for (int i = 0; i <= help; ++i) {  // the heads with many parts together, then each warp its own
+    for (int i = 0; i <= help; ++i) {  // the heads with the most parts by the whole block, then each its own
       const bool together = i < help;
-      if (together ? parts[i].np <= ALONE : p.np == 1 || p.np > ALONE) continue;
-      Joined x = join_parts(together ? parts[i] : p, stride, c, (together ? warp * SHARE : 0) + lane / V,
-                            (together ? NW : 1) * SHARE);
+      if (together && parts[i].np <= longest) continue;
+      Joined x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      Parts of = p;  // (by value: a choice between the two places would keep p in memory)
+      if (together) of = parts[i];
+      if (together || (p.np > 1 && p.np <= longest))
+        x = join_parts(of, stride, c, (together ? warp : rank) * SHARE + lane / V,
+                       (together ? NW : each) * SHARE);
       if (SHARE > 1)  // lanes with the same channels
         x.add(__shfl_down_sync(0xffffffffu, x.m, 16), __shfl_down_sync(0xffffffffu, x.l, 16),
               make_float4(__shfl_down_sync(0xffffffffu, x.o.x, 16), __shfl_down_sync(0xffffffffu, x.o.y, 16),
                           __shfl_down_sync(0xffffffffu, x.o.z, 16), __shfl_down_sync(0xffffffffu, x.o.w, 16)));
-      if (!together) {
-        r = x;
+      if (!together && each == 1) {
+        if (p.np <= longest) r = x;
         break;
       }
       if (lane < V) so[warp][lane] = x.o;
@@ -967,11 +986,11 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedSha
         sl[warp] = x.l;
       }
       __syncthreads();
-      if (warp == i && lane < V)
-        for (int w = 0; w < NW; ++w) r.add(sm[w], sl[w], so[w][lane]);
+      if (lane < V && (together ? warp == i * each : rank == 0 && p.np <= longest))
+        for (int w = together ? 0 : warp, n = together ? NW : each; n > 0; ++w, --n) r.add(sm[w], sl[w], so[w][lane]);
       __syncthreads();
     }
-    if (!mine || p.np == 1 || lane >= V) continue;  // np == 1: its warp has written it
+    if (!mine || p.np == 1 || rank != 0 || lane >= V) continue;  // np == 1: its team has written it
     T* out = static_cast<T*>(a.out) + head * HD;
     const float f = r.l == 0.f ? 0.f : 1.f / r.l;
     out[c] = from_f<T>(r.o.x * f);
@@ -985,39 +1004,44 @@ int units_of(const PagedShape& s, int heads) {  // units of a sequence
   const int group = s.H / s.Hkv;
   return s.Hkv * ((group + heads - 1) / heads);
 }
-// Query heads of a unit: as many of a key/value head's as a tile takes.
-int tile_heads(const PagedShape& s) {
-  if (s.dtype == 0) return 4;
-  return s.H / s.Hkv > 8 ? 16 : s.H / s.Hkv > 4 ? 8 : 4;
+// Query heads of a unit: as many of a key/value head's as a tile takes, or two or
+// four tiles of a team where there are more.
+int unit_heads(const PagedShape& s) {
+  const int group = s.H / s.Hkv, most = s.dtype == 0 ? 16 : 32;
+  int n = 4;
+  while (n < group && n < most) n *= 2;
+  return n;
 }
 constexpr int MAX_WARPS = 12;  // of an SM, at most
 
-template <typename T, int HD, typename Tile, int NW, int STAGES, int OCC>
+template <typename T, int HD, typename Tile, int TW, int NW, int STAGES, int OCC>
 cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   static_assert(NW * OCC <= MAX_WARPS, "the workspace holds the parts of MAX_WARPS warps an SM");
+  constexpr int TEAMS = NW / TW;
   const int group = s.H / s.Hkv;
-  a.heads = group < Tile::HEADS ? group : Tile::HEADS;
-  a.units = units_of(s, Tile::HEADS);
+  a.heads = group < TW * Tile::HEADS ? group : TW * Tile::HEADS;
+  a.units = units_of(s, TW * Tile::HEADS);
   // steps there can be at most, from the sizes alone
   int64_t keys = (int64_t)s.max_pages * s.page_size;
   if (s.window > 0 && s.window + KSTEP < keys) keys = s.window + KSTEP;
   const int64_t steps = ((keys + KSTEP - 1) / KSTEP + UNIT_COST) * a.units * s.B;
-  const int64_t most = (steps + NW * MIN_COST - 1) / (NW * MIN_COST);
-  constexpr size_t smem = (size_t)NW * (STAGES * 2 * KSTEP * HD * sizeof(T) + Tile::WARP_BYTES + 2 * HD * sizeof(T) +
-                                        HD / 2 * sizeof(float2));
-  static_assert((smem + sizeof(Plan<NW * 32>) + 1024) * OCC <= 228 * 1024, "OCC blocks share an SM's memory");
-  auto kern = paged_decode_kernel<T, HD, Tile, NW, STAGES, OCC>;
+  const int64_t most = (steps + TEAMS * MIN_COST - 1) / (TEAMS * MIN_COST);
+  constexpr size_t smem = (size_t)TEAMS * STAGES * 2 * KSTEP * HD * sizeof(T) +
+                          (size_t)NW * (Tile::WARP_BYTES + 2 * HD * sizeof(T) + HD / 2 * sizeof(float2));
+  static_assert((smem + sizeof(Plan<NW * 32, TEAMS>) + 1024) * OCC <= 228 * 1024, "OCC blocks share an SM's memory");
+  auto kern = paged_decode_kernel<T, HD, Tile, TW, NW, STAGES, OCC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   int64_t grid = (int64_t)num_sms() * OCC;
   if (grid > most) grid = most;
-  a.warps = (int)grid * NW;
-  a.inv_warps = 1.0 / a.warps;
+  a.teams = (int)grid * TEAMS;
+  a.inv_teams = 1.0 / a.teams;
   e = launch_dependent(kern, dim3((unsigned)grid), NW * 32, smem, st, s, a, rope_freqs(HD, s.log2_base));
   if (e != cudaSuccess) return e;
   // the join: scheduled as the first kernel ends, its blocks wait for that before they read a part
   const int64_t heads = (int64_t)s.B * s.H, blocks = 2 * num_sms();
-  int per_block = (int)((heads + blocks - 1) / blocks < JOIN_WARPS ? (heads + blocks - 1) / blocks : JOIN_WARPS);
+  int per_block = 1;  // heads of a block: 1, 2, 4 or 8
+  while (per_block < JOIN_WARPS && per_block * blocks < heads) per_block *= 2;
   const int64_t need = (heads + per_block - 1) / per_block;
   return launch_dependent(paged_join_kernel<T, HD>, dim3((unsigned)(need < blocks ? need : blocks)), JOIN_WARPS * 32, 0,
                           st, s, a, per_block);
@@ -1026,8 +1050,9 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
 }  // namespace
 
 size_t paged_decode_workspace_bytes(const PagedShape& s) {
-  const int group = s.H / s.Hkv, most = tile_heads(s);
-  return (size_t)num_sms() * MAX_WARPS * 2 * (group < most ? group : most) * PART_ROW * sizeof(float);
+  const int group = s.H / s.Hkv, most = unit_heads(s), warps = most / (s.dtype == 0 ? 4 : 8);  // of a team
+  return (size_t)num_sms() * (MAX_WARPS / (warps > 1 ? warps : 1)) * 2 * (group < most ? group : most) * PART_ROW *
+         sizeof(float);
 }
 
 cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const void* q, const void* k, const void* v,
@@ -1049,17 +1074,29 @@ cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const v
   a.shift = log2_of(s.page_size);
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)s.hd);
   a.err = err;
-  const int heads = tile_heads(s);
-  if (s.dtype == 1 && s.hd == 128)
-    return heads == 4   ? run<bf16, 128, MmaTile<128, 1>, 4, 2, 2>(s, a, st)
-           : heads == 8 ? run<bf16, 128, MmaTile<128, 2>, 4, 2, 2>(s, a, st)
-                        : run<bf16, 128, MmaTile<128, 4>, 4, 2, 2>(s, a, st);
-  if (s.dtype == 1 && s.hd == 64)
-    return heads == 4   ? run<bf16, 64, MmaTile<64, 1>, 4, 2, 3>(s, a, st)
-           : heads == 8 ? run<bf16, 64, MmaTile<64, 2>, 4, 3, 2>(s, a, st)
-                        : run<bf16, 64, MmaTile<64, 4>, 4, 3, 2>(s, a, st);
-  if (s.dtype == 0 && s.hd == 128) return run<float, 128, SimtTile<128>, 4, 2, 1>(s, a, st);
-  if (s.dtype == 0 && s.hd == 64) return run<float, 64, SimtTile<64>, 4, 2, 2>(s, a, st);
+  const int heads = unit_heads(s);
+  if (s.dtype == 1 && s.hd == 128) {
+    if (heads == 4) return run<bf16, 128, MmaTile<128, 1>, 1, 4, 2, 2>(s, a, st);
+    if (heads == 8) return run<bf16, 128, MmaTile<128, 2>, 1, 4, 2, 2>(s, a, st);
+    if (heads == 16) return run<bf16, 128, MmaTile<128, 2>, 2, 4, 3, 3>(s, a, st);
+    return run<bf16, 128, MmaTile<128, 2>, 4, 4, 6, 3>(s, a, st);
+  }
+  if (s.dtype == 1 && s.hd == 64) {
+    if (heads == 4) return run<bf16, 64, MmaTile<64, 1>, 1, 4, 2, 3>(s, a, st);
+    if (heads == 8) return run<bf16, 64, MmaTile<64, 2>, 1, 4, 3, 2>(s, a, st);
+    if (heads == 16) return run<bf16, 64, MmaTile<64, 2>, 2, 4, 4, 3>(s, a, st);
+    return run<bf16, 64, MmaTile<64, 2>, 4, 4, 6, 3>(s, a, st);
+  }
+  if (s.dtype == 0 && s.hd == 128) {
+    if (heads == 4) return run<float, 128, SimtTile<128>, 1, 4, 2, 1>(s, a, st);
+    if (heads == 8) return run<float, 128, SimtTile<128>, 2, 4, 2, 2>(s, a, st);
+    return run<float, 128, SimtTile<128>, 4, 4, 3, 2>(s, a, st);
+  }
+  if (s.dtype == 0 && s.hd == 64) {
+    if (heads == 4) return run<float, 64, SimtTile<64>, 1, 4, 2, 2>(s, a, st);
+    if (heads == 8) return run<float, 64, SimtTile<64>, 2, 4, 3, 3>(s, a, st);
+    return run<float, 64, SimtTile<64>, 4, 4, 4, 3>(s, a, st);
+  }
   return cudaErrorInvalidValue;
 }
 
