@@ -1090,7 +1090,7 @@ cudaError_t launch_paged_decode(const PagedShape& s, const int64_t* pos, const v
   if (s.dtype == 0 && s.hd == 128) {
     if (heads == 4) return run<float, 128, SimtTile<128>, 1, 4, 2, 1>(s, a, st);
     if (heads == 8) return run<float, 128, SimtTile<128>, 2, 4, 2, 2>(s, a, st);
-    return run<float, 128, SimtTile<128>, 4, 4, 3, 2>(s, a, st);
+    return run<float, 128, SimtTile<128>, 4, 4, 2, 3>(s, a, st);
   }
   if (s.dtype == 0 && s.hd == 64) {
     if (heads == 4) return run<float, 64, SimtTile<64>, 1, 4, 2, 2>(s, a, st);
