@@ -25,11 +25,11 @@
 // the keys: the same bits whatever ran first, and no block waits for another.
 //
 // Measured (one B200, GPU time in a graph; share of the bytes' time at 6535 GB/s):
-//   64 sequences of 64..4096, 10 heads of 128, bf16          109.2 us  0.96
-//   8 of 8192..65536, 32 query heads on 4 of 128, bf16        98.8 us  0.94
+//   64 sequences of 64..4096, 10 heads of 128, bf16          109.5 us  0.95
+//   8 of 8192..65536, 32 query heads on 4 of 128, bf16        98.6 us  0.94
 //   64 of 128..8192, window 512, 10 of 128, bf16              34.3 us  0.74
-//   2 of 15005, 30010, 8 on 4 heads of 64, fp32               24.4 us  0.58
-//   1 of 190, 10 of 128, bf16                                  7.5 us  (latency)
+//   2 of 15005, 30010, 8 on 4 heads of 64, fp32               24.1 us  0.58
+//   1 of 190, 10 of 128, bf16                                  7.4 us  (latency)
 // Beside the streaming each call pays about 3.5 us from the launch to the first data
 // (positions, page numbers and entries are three loads that depend on one another),
 // 2 us for the join, and what the slowest SM takes longer than the average (3 to 8 us).

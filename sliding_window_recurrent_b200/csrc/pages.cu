@@ -22,8 +22,8 @@ namespace {
 // plan (one block: prefix sums over the requests) takes one barrier a sum, the
 // fill (a thread per token row) finds its requests by block-wide counts instead of a
 // chain of probes, and is scheduled while the plan runs. Up to ONE_LAUNCH_ROWS rows
-// the plan's block does the rows itself. GPU time: 64 single tokens 3.2 us, 96
-// prompts and ends (74 k rows) 6.0 us, 2048 requests (52 k rows) 10.4 us.
+// the plan's block does the rows itself. GPU time: 64 single tokens 3.0 us, 96
+// prompts and ends (74 k rows) 5.7 us, 2048 requests (52 k rows) 10.2 us.
 // ---------------------------------------------------------------------------
 struct PlanTotals {
   int64_t n_old, avail, left;  // free pages before, with the returned ones, after
