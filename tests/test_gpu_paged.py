@@ -668,6 +668,40 @@ def test_calls_follow_their_producers_and_precede_their_consumers():
     assert mg.maglev_device_status() == 0
 
 
+def test_captured_behind_copies_fills_and_other_streams():
+    """In a graph the calls follow memory copies, fills and kernels of a stream that was forked off and joined again;
+    replays with changed sources give what separate calls give."""
+    s = Step(41, [700, 33, 0, 128], 4, 2, 128, 16)
+    s.run()
+    torch.cuda.synchronize()
+    sources = [(normal(generator(50 + i), s.q.shape, "bf16"), normal(generator(60 + i), s.k.shape, "bf16")) for i in range(3)]
+    want = []
+    for q, k in sources:
+        s.q.copy_(q)
+        s.k.copy_(k)
+        want.append(s.run().clone())
+    torch.cuda.synchronize()
+    src_q, src_k, result = sources[0][0].clone(), sources[0][1].clone(), torch.empty_like(s.out)
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        s.out.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            s.k.copy_((src_k.float() * 1).to(s.k.dtype))
+        s.q.copy_(src_q)
+        torch.cuda.current_stream().wait_stream(side)
+        s.run()
+        result.copy_(s.out)
+        s.q.zero_()
+    for i in (0, 1, 2, 1):
+        src_q.copy_(sources[i][0])
+        src_k.copy_(sources[i][1])
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(result, want[i]), i
+
+
 def test_workspace_may_serve_layers_of_other_shapes():
     """One workspace, sized for the largest and with any content, for layers of different head counts and types in
     turn."""
