@@ -43,11 +43,10 @@
 // Eight warps with two 8 KB stages each (128 KB in flight on an SM) are what HBM
 // needs; with twelve the SMs' shares drift apart and the slowest ends 20% late.
 #include "paged.cuh"
+#include "paged_grid.h"
 
 namespace maglev {
 namespace {
-
-constexpr int KSTEP = 16;  // keys of a step
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 // 16 bytes to shared memory; bytes = 0 fills with zeros and reads nothing.
@@ -504,13 +503,6 @@ struct DecodeArgs {
 };
 
 constexpr int PART_M = 128, PART_ROW = 132;  // a part's row: up to 128 channels, then m and l
-// A unit counts as this many steps more than it has: its query, its new entry and
-// its end keep a warp from its copies for about that time, and a warp dealt only
-// short units ended last (64 sequences of 64 to 4096: 108 us, 96 on average; 512
-// of up to 190: 72, 66, 61, 61 us in all with 1, 2, 3, 4).
-constexpr int UNIT_COST = 3;
-constexpr int MIN_COST = 1;  // least of a warp's range
-
 // Position, first key, first step and cost of one unit of sequence b (cost 0: not
 // running). Its steps are the last cost - UNIT_COST of the cost's.
 struct Sequence {
@@ -578,7 +570,6 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS, TEAMS>& plan, const Pag
   // total / teams, rounded up (a 64-bit division would take 0.3 us here)
   r.per = r.total > 0 ? (int64_t)((double)(r.total - 1) * a.inv_teams) + 1 : 1;
   if (r.per * a.teams < r.total) ++r.per;
-  if (r.per < MIN_COST) r.per = MIN_COST;
   at *= a.units;
   mine *= a.units;
 #pragma unroll
@@ -1023,19 +1014,13 @@ cudaError_t run(const PagedShape& s, DecodeArgs a, cudaStream_t st) {
   const int group = s.H / s.Hkv;
   a.heads = group < TW * Tile::HEADS ? group : TW * Tile::HEADS;
   a.units = units_of(s, TW * Tile::HEADS);
-  // steps there can be at most, from the sizes alone
-  int64_t keys = (int64_t)s.max_pages * s.page_size;
-  if (s.window > 0 && s.window + KSTEP < keys) keys = s.window + KSTEP;
-  const int64_t steps = ((keys + KSTEP - 1) / KSTEP + UNIT_COST) * a.units * s.B;
-  const int64_t most = (steps + TEAMS * MIN_COST - 1) / (TEAMS * MIN_COST);
   constexpr size_t smem = (size_t)TEAMS * STAGES * 2 * KSTEP * HD * sizeof(T) +
                           (size_t)NW * (Tile::WARP_BYTES + 2 * HD * sizeof(T) + HD / 2 * sizeof(float2));
   static_assert((smem + sizeof(Plan<NW * 32, TEAMS>) + 1024) * OCC <= 228 * 1024, "OCC blocks share an SM's memory");
   auto kern = paged_decode_kernel<T, HD, Tile, TW, NW, STAGES, OCC>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  int64_t grid = (int64_t)num_sms() * OCC;
-  if (grid > most) grid = most;
+  const int64_t grid = decode_blocks(s.B, a.units, s.max_pages, s.page_size, s.window, TEAMS, (int64_t)num_sms() * OCC);
   a.teams = (int)grid * TEAMS;
   a.inv_teams = 1.0 / a.teams;
   e = launch_dependent(kern, dim3((unsigned)grid), NW * 32, smem, st, s, a, rope_freqs(HD, s.log2_base));

@@ -422,6 +422,18 @@ def test_decode_windows(dtype, window, ps):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [2**31 - 17, 2**31 - 16, 2**31 - 1])
+def test_decode_window_without_a_limit(dtype, window):
+    """The largest windows an int holds attend to every position, as window 0 does."""
+    s = Step(13, [0, 16, 1000, 4097], 4, 2, 128, 16, dtype=dtype)
+    want = s.run().clone()
+    s.desc.window = s.window = window
+    s.out.zero_()
+    run_checked(s)
+    assert torch.equal(s.out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("ps,hd", [(16, 128), (32, 64), (256, 128)])
 def test_decode_injected(dtype, shared, ps, hd):
