@@ -452,9 +452,9 @@ size_t maglev_decode_workspace_bytes(const maglev_decode_desc* desc);
  *     (the calls below skip both). May be NULL when n_tokens == 0.
  *   workspace: maglev_page_tables_workspace_bytes(desc) bytes of scratch.
  * Errors: INVALID_ARG (sizes, NULL or misaligned pointers, pad > 0 with n_tokens
- * != B * pad), UNSUPPORTED (B * max_pages >= 2^31, max_pages * page_size
- * > 2^30 or n_tokens > 2^30). B == 0
- * enqueues nothing. */
+ * != B * pad), UNSUPPORTED (B * max_pages >= 2^31, B > 2^30, max_pages *
+ * page_size > 2^30 or n_tokens > 2^30). B == 0 enqueues nothing and writes
+ * nothing. */
 maglev_status maglev_page_tables(const maglev_paged_desc* desc, const int64_t* ctx_len, const int64_t* new_len,
                                  int64_t n_tokens, int64_t pad, int32_t* free_pages, const int32_t* n_free,
                                  int32_t* block_table, int64_t* seq_len, int32_t* n_free_out,

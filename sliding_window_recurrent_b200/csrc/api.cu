@@ -957,6 +957,8 @@ static maglev_status check_pages(const maglev_paged_desc* d) {
     return fail(MAGLEV_ERR_INVALID_ARG, "max_pages and num_pages must be >= 1");
   if ((int64_t)d->B * d->max_pages >= (int64_t)1 << 31)
     return fail(MAGLEV_ERR_UNSUPPORTED, "B * max_pages must be below 2^31");
+  // the kernels step over the sequences in int, by up to 2048 at a time
+  if (d->B > 1 << 30) return fail(MAGLEV_ERR_UNSUPPORTED, "B must be at most 2^30");
   if ((int64_t)d->max_pages * d->page_size > (int64_t)1 << 30)
     return fail(MAGLEV_ERR_UNSUPPORTED, "positions beyond 2^30 are unsupported (max_pages * page_size)");
   return MAGLEV_OK;

@@ -231,3 +231,13 @@ def test_workspace_sizes():
     assert mg.maglev_page_tables_workspace_bytes(desc()) > 0
     assert mg.maglev_page_tables_workspace_bytes(desc(page_size=20)) == 0
     assert mg.maglev_paged_decode_workspace_bytes(desc(hd=96)) == 0
+
+
+@pytest.mark.parametrize("call", [tables, write, step])
+@pytest.mark.parametrize("B", [(1 << 30) + 1, 2**31 - 1])
+def test_more_sequences_than_32_bit_loops_can_step_over_are_refused(call, B):
+    """The kernels step over the sequences in strides of up to 2048 in int: near 2^31 the last step would wrap."""
+    refused(call, UNS, "2^30", desc(B=B, max_pages=1))
+    assert mg.maglev_page_tables_workspace_bytes(desc(B=B, max_pages=1)) == 0
+    assert mg.maglev_paged_decode_workspace_bytes(desc(B=B, max_pages=1)) == 0
+    assert mg.maglev_page_tables_workspace_bytes(desc(B=1 << 30, max_pages=1)) > 0
