@@ -45,8 +45,11 @@ inline int log2_of(int x) {  // of a power of two
 
 // Launches a kernel whose blocks may be scheduled before the stream's last kernel
 // has ended (programmatic dependent launch). Every thread of it calls
-// wait_for_last() before it touches what earlier work reads or writes. Called one
-// after another, without a graph, such calls follow each other 2 to 4 us sooner.
+// wait_for_last() before it touches what earlier work reads or writes, and takes its
+// pointers without __restrict__: the inputs may still be written while its first blocks
+// wait, and const __restrict__ would promise that nothing writes them while it runs (loads
+// through the read-only path, or from before the wait). Called one after another,
+// without a graph, such calls follow each other 2 to 4 us sooner.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kern)(Params...), dim3 blocks, unsigned threads, size_t smem, cudaStream_t st,
                              const Args&... args) {

@@ -357,9 +357,8 @@ __device__ __forceinline__ void store_raw8(T* p, const Raw8<T>& r) {
 template <typename T, int HD, int MODE>
 __global__ void __launch_bounds__(WRITE_THREADS, sizeof(T) == 2 ? 3 : 2) paged_write_kernel(
     PagedShape s, const __grid_constant__ RopeFreqs rf, int shift, int64_t n, int tile, int heads, int pass,
-    const int64_t* __restrict__ slots, const int64_t* __restrict__ pos, const T* __restrict__ k,
-    const T* __restrict__ v, const T* __restrict__ Rk, const T* __restrict__ Rv, const float* __restrict__ gates,
-    T* __restrict__ kp, T* __restrict__ vp, int* err) {
+    const int64_t* slots, const int64_t* pos, const T* k, const T* v, const T* Rk, const T* Rv, const float* gates, T* kp,
+    T* vp, int* err) {
   constexpr int HALF = HD / 2, TPR = HD / 16;
   __shared__ float2 turn[MODE == WRITE_COPY ? 1 : WRITE_TURNS];
   const int64_t t0 = (int64_t)blockIdx.x * tile;

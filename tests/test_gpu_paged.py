@@ -680,6 +680,74 @@ def test_calls_follow_their_producers_and_precede_their_consumers():
     assert mg.maglev_device_status() == 0
 
 
+def test_chained_calls_read_what_the_call_before_wrote():
+    """Tables, write and step one behind the other on a side stream, with nothing between them and with different lengths,
+    rows and pages every time: a write that read its slots, positions or rows too early would leave the poison that
+    they and the pools held. Outputs and pools equal those of the same calls with a synchronisation after each."""
+    B, ps, rows, H, H_kv, hd = 3, 16, 64, 4, 2, 64
+    r = np.random.Generator(np.random.Philox(12))
+    gen = generator(12)
+    rounds = []
+    for _ in range(30):
+        new = r.multinomial(rows, [0.3, 0.5, 0.2])
+        rounds.append((torch.from_numpy(new).cuda(), torch.randperm(20, generator=gen, device="cuda").int(),
+                       [normal(gen, (rows, H_kv, hd), "bf16") for _ in range(2)], normal(gen, (B, H, hd), "bf16")))
+    ones = torch.ones(B, dtype=torch.int64, device="cuda")
+    slow = torch.randn(3000, 2999, device="cuda")
+    side = torch.cuda.Stream()
+
+    def run_all(apart):
+        T = PageTables(B, ps, 8, 20, rows)
+        L = PagedLayerState(T, H, hd, H_kv)
+        k, v, q = (torch.empty_like(x) for x in (*rounds[0][2], rounds[0][3]))
+        results = []
+
+        def then():
+            if apart:
+                torch.cuda.synchronize()
+
+        for new, order, (kn, vn), qn in rounds:
+            with torch.cuda.stream(side):
+                for x in (L.k_pages, L.v_pages, k, v, q):
+                    x.fill_(float("nan"))
+                T.pos.fill_(-1)
+                T.slots.fill_(-1)
+                T.lengths.zero_()
+                T.n_free.fill_(20)
+                T.free_pages.copy_(order)
+                T.block_table.fill_(-1)
+                zero = (slow @ slow.T)[:1, :1].to(torch.bfloat16) * 0  # some 100 us, so that the calls queue up behind it
+                q.copy_(qn + zero)
+                v.copy_(vn + zero)
+                k.copy_(kn + zero)  # the last kernel before the calls
+                then()
+                pos, slots = T.step(new, rows)
+                then()
+                L.write(slots, pos, k, v)
+                then()
+                prompt = slots.clone(), L.k_pages.clone()
+                then()
+                # a token each, its rows written over before the step writes them again
+                T.step(ones, B, 1)
+                then()
+                L.write(T.slots[:B], T.pos[:B], v[:B], k[:B])
+                then()
+                prompt += (L.v_pages.clone(),)
+                then()
+                out = L.step(T.pos[:B], q, k[:B], v[:B]).clone()
+                then()
+                results.append((*prompt, out, L.k_pages.clone(), L.v_pages.clone(), T.slots.clone(), T.block_table.clone()))
+        torch.cuda.synchronize()
+        return results
+
+    for i, (got, want) in enumerate(zip(run_all(False), run_all(True))):
+        assert bool((want[0] >= 0).all()) and torch.isfinite(want[3]).all()
+        for a, b in zip(got, want):
+            assert torch.equal(a.nan_to_num(nan=7.0) if a.is_floating_point() else a,
+                               b.nan_to_num(nan=7.0) if b.is_floating_point() else b), i
+    assert mg.maglev_device_status() == 0
+
+
 def test_captured_behind_copies_fills_and_other_streams():
     """In a graph the calls follow memory copies, fills and kernels of a stream that was forked off and joined again;
     replays with changed sources give what separate calls give."""

@@ -241,3 +241,19 @@ def test_more_sequences_than_32_bit_loops_can_step_over_are_refused(call, B):
     assert mg.maglev_page_tables_workspace_bytes(desc(B=B, max_pages=1)) == 0
     assert mg.maglev_paged_decode_workspace_bytes(desc(B=B, max_pages=1)) == 0
     assert mg.maglev_page_tables_workspace_bytes(desc(B=1 << 30, max_pages=1)) > 0
+
+
+def test_dependent_kernels_promise_nothing_about_their_inputs():
+    """A kernel that may be scheduled while its inputs are still being written must not declare them __restrict__:
+    const __restrict__ says that nothing writes them while it runs, and lets the compiler read them through the
+    read-only path and before the wait."""
+    import os
+    import re
+    seen = 0
+    for path in _build.sources():
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        if "launch_dependent(" in text:
+            seen += 1
+            assert "__restrict__" not in text and "__ldg(" not in text, os.path.basename(path)
+    assert seen == 2
