@@ -436,7 +436,10 @@ size_t maglev_decode_workspace_bytes(const maglev_decode_desc* desc);
  *     length ctx_len + new_len; another keeps its length and row.
  *   new_len[b] < 0: it is finished. Its pages go back on the free stack (in
  *     order of request and column) before any page is handed out; its length
- *     becomes 0. Its row is left as it was.
+ *     becomes 0. Its row is left as it was. A row whose length lies outside it
+ *     gives nothing back.
+ *   A ctx_len below 0 or above max_pages * page_size is recorded as
+ *     MAGLEV_ERR_BOUNDS whatever new_len is; such a request is not served.
  *   n_tokens, pad: token rows. pad == 0: packed, token i of request b is row
  *     cu_tokens[b] + i; a request whose rows end beyond n_tokens is not served.
  *     pad >= 1: row b * pad + i, n_tokens == B * pad; one with new_len > pad is

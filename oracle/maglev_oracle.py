@@ -461,8 +461,8 @@ def page_tables(ctx_len, new_len, n_tokens, pad, page_size, free, block_table):
     """Pages and token rows of one serving step, request by request.
 
     free: the free pages, last one handed out first; block_table [B, columns].
-    A finished request (new < 0) first gives back its ceil(ctx / page_size) pages;
-    then requests in order get ceil((ctx + new) / page_size) - ceil(ctx / page_size)
+    A finished request (new < 0) first gives back its ceil(ctx / page_size) pages
+    (nothing if its length lies outside its row); then requests in order get ceil((ctx + new) / page_size) - ceil(ctx / page_size)
     pages while the pages asked for so far fit. Returns a dict: the table, the
     free list, lengths, prefix sums of the token counts (at most n_tokens),
     positions and slots of the token rows (-1 without one). Inputs are not modified.
@@ -476,7 +476,8 @@ def page_tables(ctx_len, new_len, n_tokens, pad, page_size, free, block_table):
     lens = list(ctx)
     for b in range(B):
         if new[b] < 0:
-            stack += [int(x) for x in table[b, :pages(ctx[b])]]
+            if 0 <= ctx[b] <= columns * page_size:
+                stack += [int(x) for x in table[b, :pages(ctx[b])]]
             lens[b] = 0
     budget, asked, rows = len(stack), 0, 0
     cu = [0]

@@ -216,15 +216,15 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
   const int cap = a.max_pages << shift;  // at most 2^30, like n_tokens
   const uint32_t most = (uint32_t)a.n_tokens + 1;
   auto pages_of = [&](int len) { return (len + a.page_size - 1) >> shift; };
-  // a length outside its row is cut for what it holds, and never served (cap + 1)
+  // a request with a length outside its row is not served (cap + 1), and gives nothing back
   auto clip = [&](int64_t c) { return c < 0 || c > cap ? cap + 1 : (int)c; };
-  auto held_of = [&](int64_t c) { return pages_of(c < 0 ? 0 : (c > cap ? cap : (int)c)); };
+  auto held_of = [&](int c) { return c > cap ? 0 : pages_of(c); };
   int n_old = *a.n_free, released = 0;
   if (a.B > chunk) {  // pages come back before any is handed out
     uint2 total;
     uint32_t rel = 0;
     for (int b = tid; b < a.B; b += blockDim.x)
-      if (a.new_len[b] < 0) rel += held_of(a.ctx_len[b]);
+      if (a.new_len[b] < 0) rel += held_of(clip(a.ctx_len[b]));
     block_exclusive(make_uint2(0, rel), most, sums[3], &total);
     released = total.y;
   }
@@ -243,11 +243,12 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
       const int64_t n = in ? a.new_len[b0 + e] : 0;
       ctx[e] = in ? a.ctx_len[b0 + e] : 0;
       c[e] = clip(ctx[e]);
-      held[e] = held_of(ctx[e]);
+      held[e] = held_of(c[e]);
       done[e] = n < 0;
       rows[e] = n < 0 ? 0 : (n > a.n_tokens ? most : (uint32_t)n);
       v.x = min(v.x + rows[e], most);
       v.y += done[e] ? held[e] : 0;
+      if (c[e] > cap) record_error(err, DEV_BOUNDS);
     }
     if (base > 0) __syncthreads();  // the sums of the last chunk have been read
     uint2 at = block_exclusive(v, most, sums[0], &total);

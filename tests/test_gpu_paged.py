@@ -162,6 +162,25 @@ def test_page_tables_many_returned_pages():
         t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table))
 
 
+@pytest.mark.parametrize("B", [3, 2050])
+@pytest.mark.parametrize("new", [-1, 0, 1])
+@pytest.mark.parametrize("length", [-5, 33, 1 << 40])
+def test_page_tables_record_a_bad_length_alone(B, new, length):
+    """A length outside its row, with nothing else wrong: recorded; a running request is not served, a finished one gives
+    nothing back (its row would name pages that it does not hold)."""
+    table = np.full((B, 2), -1, dtype=np.int32)
+    table[1] = [3, 4]
+    lens, news = np.zeros(B, dtype=np.int64), np.zeros(B, dtype=np.int64)
+    lens[1], news[1] = length, new
+    t = Tables(lens, news, 4, 0, 16, [2], table, 6)
+    t.run()
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS
+    assert t.n_out.tolist() == [1] and t.free.tolist() == [2] + [-7] * 5
+    assert t.seq_len[1].item() == (0 if new < 0 else length) and (t.pos == -1).all() and (t.slots == -1).all()
+    np.testing.assert_array_equal(t.table.cpu().numpy(), table)
+
+
 def test_page_tables_without_token_rows():
     """Only ends and idle requests: no rows, pos and slots NULL; requests with tokens find no room and stay."""
     table = np.array([[4, 2], [3, -1], [0, -1]], dtype=np.int32)

@@ -67,6 +67,13 @@ def test_page_tables_order_and_refusals():
     assert got["seq_len"].tolist() == [0, 4, 4] and got["free"] == [3]
 
 
+def test_page_tables_take_nothing_from_a_row_of_a_bad_length():
+    """Hand-worked: a finished row whose length lies outside it puts nothing on the stack."""
+    table = np.array([[2, 3, 4, -1], [0, 10, 11, 12], [5, 6, 7, 8]])
+    got = oracle.page_tables([65, -1, 64], [-1] * 3, 0, 0, 16, [13], table)
+    assert got["free"] == [13, 5, 6, 7, 8] and got["seq_len"].tolist() == [0] * 3
+
+
 def _paged_from_forward(seed, T, H, hd, W, ps, inject):
     """A forward pass's entries of one sequence in scattered pages, and what went into it."""
     r = rng(seed)
