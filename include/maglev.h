@@ -436,8 +436,12 @@ size_t maglev_decode_workspace_bytes(const maglev_decode_desc* desc);
  *     length ctx_len + new_len; another keeps its length and row.
  *   new_len[b] < 0: it is finished. Its pages go back on the free stack (in
  *     order of request and column) before any page is handed out; its length
- *     becomes 0. Its row is left as it was. A row whose length lies outside it
- *     gives nothing back.
+ *     becomes 0. Its row is left as it was. The row's first columns, as far as
+ *     they are negative, give nothing back: a caller who frees pages that a
+ *     window has passed puts them on the stack and sets their columns to -1.
+ *     Another number outside the pool is recorded as MAGLEV_ERR_BOUNDS, and -1
+ *     takes its place on the stack (handed out, it gives no slots and is
+ *     recorded again). A row whose length lies outside it gives nothing back.
  *   A ctx_len below 0 or above max_pages * page_size is recorded as
  *     MAGLEV_ERR_BOUNDS whatever new_len is; such a request is not served.
  *   n_tokens, pad: token rows. pad == 0: packed, token i of request b is row

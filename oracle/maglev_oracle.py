@@ -457,12 +457,14 @@ def decode_step(pos, q, k, v, krec_rot, vrec, gate_logits, k_ring, v_ring,
 # --------------------------------------------------------------------------
 # Paged key/value cache
 # --------------------------------------------------------------------------
-def page_tables(ctx_len, new_len, n_tokens, pad, page_size, free, block_table):
+def page_tables(ctx_len, new_len, n_tokens, pad, page_size, free, block_table, num_pages=None):
     """Pages and token rows of one serving step, request by request.
 
     free: the free pages, last one handed out first; block_table [B, columns].
     A finished request (new < 0) first gives back its ceil(ctx / page_size) pages
-    (nothing if its length lies outside its row); then requests in order get ceil((ctx + new) / page_size) - ceil(ctx / page_size)
+    (not the row's first columns where they are negative: given back before; -1 in
+    the place of another number outside the pool of num_pages; nothing if its
+    length lies outside its row); then requests in order get ceil((ctx + new) / page_size) - ceil(ctx / page_size)
     pages while the pages asked for so far fit. Returns a dict: the table, the
     free list, lengths, prefix sums of the token counts (at most n_tokens),
     positions and slots of the token rows (-1 without one). Inputs are not modified.
@@ -477,7 +479,9 @@ def page_tables(ctx_len, new_len, n_tokens, pad, page_size, free, block_table):
     for b in range(B):
         if new[b] < 0:
             if 0 <= ctx[b] <= columns * page_size:
-                stack += [int(x) for x in table[b, :pages(ctx[b])]]
+                held = [int(x) for x in table[b, :pages(ctx[b])]]
+                lead = next((c for c, x in enumerate(held) if x >= 0), len(held))
+                stack += [x if x >= 0 and (num_pages is None or x < num_pages) else -1 for x in held[lead:]]
             lens[b] = 0
     budget, asked, rows = len(stack), 0, 0
     cu = [0]

@@ -10,8 +10,9 @@ namespace maglev {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Page tables. A finished request (new < 0) gives its held(b) =
-// ceil(ctx / page_size) pages back; the others need need(b) =
+// Page tables. A finished request (new < 0) gives the pages of its held(b) =
+// ceil(ctx / page_size) columns back, from the first that is not negative on (the ones
+// before it were given back when a window had passed them); the others need need(b) =
 // ceil((ctx + new) / page_size) - held(b). With the stack of free pages
 // S = free[0..n) followed by the returned pages, request b is served when the
 // inclusive prefix sum of need up to b is at most |S| (or need(b) == 0), and
@@ -22,8 +23,8 @@ namespace {
 // plan (one block: prefix sums over the requests) takes one barrier a sum, the
 // fill (a thread per token row) finds its requests by block-wide counts instead of a
 // chain of probes, and is scheduled while the plan runs. Up to ONE_LAUNCH_ROWS rows
-// the plan's block does the rows itself. GPU time: 64 single tokens 3.0 us, 96
-// prompts and ends (74 k rows) 5.7 us, 2048 requests (52 k rows) 10.2 us.
+// the plan's block does the rows itself. GPU time: 64 single tokens 3.2 us, 96
+// prompts and ends (74 k rows) 6.0 us, 2048 requests (52 k rows) 10.6 us.
 // ---------------------------------------------------------------------------
 struct PlanTotals {
   int64_t n_old, avail, left;  // free pages before, with the returned ones, after
@@ -32,14 +33,14 @@ struct PlanTotals {
 struct PlanViews {
   PlanTotals* totals;
   int2* req;  // [B] first position of a served request's tokens (else -1), pages handed out to earlier requests
-  int2* fin;  // [finished] pages returned up to and with a finished request, and which it is
+  int4* fin;  // [finished] pages returned up to and with a finished request, which it is, its first column with a page
 };
 __device__ __forceinline__ PlanViews plan_views(void* ws, int B) {
   char* p = static_cast<char*>(ws);
   PlanViews v;
   v.totals = reinterpret_cast<PlanTotals*>(p);
-  v.req = reinterpret_cast<int2*>(p + 256);
-  v.fin = v.req + B;
+  v.fin = reinterpret_cast<int4*>(p + 256);
+  v.req = reinterpret_cast<int2*>(v.fin + B);
   return v;
 }
 
@@ -109,20 +110,44 @@ __device__ __forceinline__ void block_first_above(const int64_t* x, int n, int64
 }
 
 // Page k of the pages that finished requests return (request, then column order).
-__device__ __forceinline__ int returned_page(const PageTablesArgs& a, const int2* fin, int finished, int k) {
+__device__ __forceinline__ int returned_page(const PageTablesArgs& a, const int4* fin, int finished, int k) {
   const int i = first_above([&](int j) { return fin[j].x; }, 0, finished, k);
   if (i >= finished) return -1;
-  return a.block_table[(int64_t)fin[i].y * a.max_pages + (k - (i > 0 ? fin[i - 1].x : 0))];
+  return a.block_table[(int64_t)fin[i].y * a.max_pages + fin[i].z + (k - (i > 0 ? fin[i - 1].x : 0))];
+}
+
+// Row b's first column. Negative columns come first, so where it names a page the row is whole.
+__device__ __forceinline__ int first_column(const PageTablesArgs& a, int b) {
+  return a.block_table[(int64_t)b * a.max_pages];
+}
+// The first of row b's `held` columns that is not negative (held, if there is none), where the very first one is
+// negative: searched by 8 columns at a time.
+__device__ __forceinline__ int first_page(const PageTablesArgs& a, int b, int held) {
+  const int32_t* row = a.block_table + (int64_t)b * a.max_pages;
+  int lo = 1, len = held - 1;  // it lies in [lo, lo + len]
+  while (len > 0) {
+    const int step = (len + 7) / 8;
+    int negative = 0;  // shares [lo + u step, lo + (u + 1) step) of which even the last column is
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = (u + 1) * step - 1;
+      negative += u * step < len && row[lo + (i < len ? i : len - 1)] < 0;
+    }
+    const int before = negative * step < len ? negative * step : len;
+    lo += before;
+    len = before < len ? min(step - 1, len - before) : 0;
+  }
+  return lo;
 }
 
 // What a fill needs of the requests that its rows belong to.
 struct FillRequests {
   int end[FILL_ROWS + 1];  // where their rows end, from the fill's first row; [0]: where the first request's begin
   int2 at[FILL_ROWS];      // start, need_ex
-  int2 fin[FILL_ROWS];     // finished requests, if there are no more
+  int4 fin[FILL_ROWS];     // finished requests, if there are no more
 };
 // The finished requests, staged (a barrier has to follow before they are used).
-__device__ __forceinline__ const int2* stage_finished(const PlanViews& w, int finished, FillRequests& f) {
+__device__ __forceinline__ const int4* stage_finished(const PlanViews& w, int finished, FillRequests& f) {
   if (finished > FILL_ROWS) return w.fin;
   for (int i = threadIdx.x; i < finished; i += blockDim.x) f.fin[i] = w.fin[i];
   return f.fin;
@@ -130,7 +155,7 @@ __device__ __forceinline__ const int2* stage_finished(const PlanViews& w, int fi
 
 // Token rows [t0, t0 + FILL_ROWS) of the map, and with them the table columns whose
 // page a row is the first of.
-__device__ void fill_rows(const PageTablesArgs& a, const PlanViews& w, const PlanTotals& tot, const int2* fin, int shift,
+__device__ void fill_rows(const PageTablesArgs& a, const PlanViews& w, const PlanTotals& tot, const int4* fin, int shift,
                           int64_t t0, FillRequests& f, int* err) {
   const int64_t t1 = t0 + FILL_ROWS < a.n_tokens ? t0 + FILL_ROWS : a.n_tokens;
   int b0 = 0, b1 = 0;  // the requests these rows belong to
@@ -192,14 +217,19 @@ __device__ void fill_rows(const PageTablesArgs& a, const PlanViews& w, const Pla
 }
 
 // Returned pages that no request took stay on the stack: entries n_old..left-1.
-__device__ void push_returned(const PageTablesArgs& a, const PlanTotals& tot, const int2* fin, int64_t first, int64_t step,
+__device__ void push_returned(const PageTablesArgs& a, const PlanTotals& tot, const int4* fin, int64_t first, int64_t step,
                               int* err) {
   for (int64_t j = tot.n_old + first; j < tot.left; j += step) {
     if (j >= a.num_pages) {  // more pages returned than the pool has
       record_error(err, DEV_BOUNDS);
       break;
     }
-    a.free_pages[j] = returned_page(a, fin, tot.finished, (int)(j - tot.n_old));
+    int page = returned_page(a, fin, tot.finished, (int)(j - tot.n_old));
+    if (page < 0 || page >= a.num_pages) {  // of a finished row: no page of the pool
+      record_error(err, DEV_BOUNDS);
+      page = -1;
+    }
+    a.free_pages[j] = page;
   }
 }
 
@@ -223,16 +253,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
   if (a.B > chunk) {  // pages come back before any is handed out
     uint2 total;
     uint32_t rel = 0;
-    for (int b = tid; b < a.B; b += blockDim.x)
-      if (a.new_len[b] < 0) rel += held_of(clip(a.ctx_len[b]));
+    for (int b = tid; b < a.B; b += blockDim.x) {
+      if (a.new_len[b] >= 0) continue;
+      const int held = held_of(clip(a.ctx_len[b]));
+      rel += held > 0 && first_column(a, b) < 0 ? held - first_page(a, b, held) : held;
+    }
     block_exclusive(make_uint2(0, rel), most, sums[3], &total);
     released = total.y;
   }
-  uint2 before = make_uint2(0, 0);  // rows and returned pages of earlier chunks
-  uint32_t need_before = 0, fin_before = 0, taken = 0;
+  uint32_t rows_before = 0, fin_before = 0, back_before = 0, need_before = 0, taken = 0;  // of earlier chunks
   for (int base = 0; base < a.B; base += chunk) {
     const int b0 = base + tid * PLAN_EACH;
-    int c[PLAN_EACH], held[PLAN_EACH];
+    int c[PLAN_EACH], held[PLAN_EACH], lead[PLAN_EACH];  // lead: columns that a finished request's pages begin behind
     uint32_t rows[PLAN_EACH];  // one row more than there are is as bad as any number of them
     bool done[PLAN_EACH];
     int64_t ctx[PLAN_EACH];
@@ -247,14 +279,18 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
       done[e] = n < 0;
       rows[e] = n < 0 ? 0 : (n > a.n_tokens ? most : (uint32_t)n);
       v.x = min(v.x + rows[e], most);
-      v.y += done[e] ? held[e] : 0;
+      v.y += done[e];
       if (c[e] > cap) record_error(err, DEV_BOUNDS);
     }
+#pragma unroll
+    for (int e = 0; e < PLAN_EACH; ++e) lead[e] = done[e] && held[e] > 0 ? first_column(a, b0 + e) : 0;
     if (base > 0) __syncthreads();  // the sums of the last chunk have been read
     uint2 at = block_exclusive(v, most, sums[0], &total);
-    at = make_uint2(min(at.x + before.x, most), at.y + before.y);
-    before = make_uint2(min(before.x + total.x, most), before.y + total.y);
-    uint32_t end[PLAN_EACH], need[PLAN_EACH], mine = 0, ends = 0;
+    at.x = min(at.x + rows_before, most);
+    rows_before = min(rows_before + total.x, most);
+    uint32_t fin_ex = at.y + fin_before;
+    fin_before += total.y;
+    uint32_t end[PLAN_EACH], need[PLAN_EACH], mine = 0, back = 0;
     bool fits[PLAN_EACH];
 #pragma unroll
     for (int e = 0; e < PLAN_EACH; ++e) {
@@ -264,13 +300,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
                 (a.pad ? rows[e] <= a.pad : end[e] < most);
       need[e] = fits[e] ? pages_of(c[e] + (int)rows[e]) - held[e] : 0;
       mine += need[e];
-      ends += done[e];
+      lead[e] = lead[e] < 0 ? first_page(a, b0 + e, held[e]) : 0;  // its load has had the barrier's time
+      back += done[e] ? held[e] - lead[e] : 0;
     }
-    const uint2 pre = block_exclusive(make_uint2(ends, mine), ~0u, sums[1], &total);
-    uint32_t need_ex = need_before + pre.y, fin_ex = fin_before + pre.x;
+    const uint2 pre = block_exclusive(make_uint2(back, mine), ~0u, sums[1], &total);
+    uint32_t back_ex = back_before + pre.x, need_ex = need_before + pre.y;
+    back_before += total.x;
     need_before += total.y;
-    fin_before += total.x;
-    if (a.B <= chunk) released = before.y;
+    if (a.B <= chunk) released = back_before;
     if (base == 0) {
       if (n_old < 0 || n_old > a.num_pages) {
         if (tid == 0) record_error(err, DEV_BOUNDS);
@@ -284,8 +321,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
       if (b >= a.B) break;
       const bool served = fits[e] && (need[e] == 0 || (int64_t)need_ex + need[e] <= (int64_t)n_old + released);
       if (done[e]) {
-        at.y += held[e];
-        w.fin[fin_ex++] = make_int2((int)at.y, b);
+        back_ex += held[e] - lead[e];
+        w.fin[fin_ex++] = make_int4((int)back_ex, b, lead[e], 0);
       }
       a.cu_tokens[b + 1] = end[e] < most ? end[e] : a.n_tokens;
       a.seq_len[b] = done[e] ? 0 : (served ? ctx[e] + rows[e] : ctx[e]);
@@ -304,7 +341,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) page_plan_kernel(PageTablesArgs 
   }
   if (!fill) return;
   __syncthreads();  // the plan is visible to the block
-  const int2* fin = stage_finished(w, tot.finished, requests);
+  const int4* fin = stage_finished(w, tot.finished, requests);
   __syncthreads();
   for (int64_t t0 = 0; t0 < a.n_tokens; t0 += FILL_ROWS) {
     if (t0 > 0) __syncthreads();  // the requests of the last rows have been read
@@ -318,7 +355,7 @@ __global__ void __launch_bounds__(FILL_ROWS) page_fill_kernel(PageTablesArgs a, 
   const PlanViews w = plan_views(ws, a.B);
   wait_for_last();  // the plan is written
   const PlanTotals tot = *w.totals;
-  const int2* fin = stage_finished(w, tot.finished, requests);
+  const int4* fin = stage_finished(w, tot.finished, requests);
   fill_rows(a, w, tot, fin, shift, (int64_t)blockIdx.x * FILL_ROWS, requests, err);  // has a barrier before it reads fin
   push_returned(a, tot, fin, (int64_t)blockIdx.x * FILL_ROWS + threadIdx.x, (int64_t)gridDim.x * FILL_ROWS, err);
 }
@@ -497,7 +534,7 @@ constexpr int64_t ONE_LAUNCH_ROWS = 512;
 
 }  // namespace
 
-size_t page_tables_workspace_bytes(int B) { return 256 + (size_t)B * 2 * sizeof(int2); }
+size_t page_tables_workspace_bytes(int B) { return 256 + (size_t)B * (sizeof(int4) + sizeof(int2)); }
 
 int page_tables_kernels(int64_t n_tokens) { return n_tokens <= ONE_LAUNCH_ROWS ? 1 : 2; }
 

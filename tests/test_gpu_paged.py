@@ -162,6 +162,40 @@ def test_page_tables_many_returned_pages():
         t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table))
 
 
+@pytest.mark.parametrize("B,ps,columns,take", [(5, 16, 4, 0.5), (9, 16, 40, 0.9), (40, 16, 600, 0.3), (96, 64, 64, 0.8),
+                                               (2048, 16, 20, 0.7), (2500, 16, 9, 1.0), (1, 16, 5000, 0.6)])
+@pytest.mark.parametrize("many_rows", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_page_tables_of_rows_that_gave_pages_back_before(B, ps, columns, take, many_rows, in_place):
+    """Finished requests whose first columns hold no page any more (negative) give back the others, in order, over one and
+    over two launches; `take` of what is there then is handed out again."""
+    r = np.random.Generator(np.random.Philox(B + columns + many_rows))
+    cap = columns * ps
+    lens = r.integers(1, cap + 1, B)
+    new = np.full(B, -1, dtype=np.int64)
+    new[B // 3::3] = 0
+    held = -(-lens // ps)
+    pool = int(held.sum()) + 4
+    order = r.permutation(pool).astype(np.int32)
+    table = np.full((B, columns), -1, dtype=np.int32)
+    for b in range(B):
+        table[b, :held[b]] = order[held[:b].sum():held[:b + 1].sum()]
+    for b in np.flatnonzero(new < 0):
+        if b % 3 != 1:
+            table[b, :r.integers(0, held[b] + 1)] = -1 - 4 * (b % 2)  # what a window has passed
+    back = int((table[new < 0] >= 0).sum())
+    idle = np.flatnonzero(new == 0)
+    lens[idle] = 0  # empty rows that ask for `take` of the pages between them
+    for i, b in enumerate(idle):
+        new[b] = min(cap, int((back + 4) * take) // len(idle) * ps - (0 if many_rows else ps - 1))
+        new[b] = max(new[b], 0)
+    n_tokens = int(new[new > 0].sum()) if many_rows else min(500, int(new[new > 0].sum()))
+    free = [int(x) for x in order[pool - 4:]]
+    t = Tables(lens, new, n_tokens, 0, ps, free, table, pool)
+    t.run(in_place=in_place)
+    t.check(oracle.page_tables(lens, new, n_tokens, 0, ps, free, table, pool), in_place)
+
+
 @pytest.mark.parametrize("B", [3, 2050])
 @pytest.mark.parametrize("new", [-1, 0, 1])
 @pytest.mark.parametrize("length", [-5, 33, 1 << 40])
@@ -179,6 +213,31 @@ def test_page_tables_record_a_bad_length_alone(B, new, length):
     assert t.n_out.tolist() == [1] and t.free.tolist() == [2] + [-7] * 5
     assert t.seq_len[1].item() == (0 if new < 0 else length) and (t.pos == -1).all() and (t.slots == -1).all()
     np.testing.assert_array_equal(t.table.cpu().numpy(), table)
+
+
+@pytest.mark.parametrize("B", [3, 2050])
+@pytest.mark.parametrize("bad", [-1, 6, 1 << 30])
+def test_page_tables_keep_numbers_outside_the_pool_off_the_stack(B, bad):
+    """A finished row that names no page behind its first one: recorded, its place on the stack holds -1; handed out
+    again it gives no slot."""
+    table = np.full((B, 3), -1, dtype=np.int32)
+    table[1] = [3, bad, 4]
+    lens, news = np.zeros(B, dtype=np.int64), np.zeros(B, dtype=np.int64)
+    lens[1], news[1] = 48, -1
+    t = Tables(lens, news, 0, 0, 16, [2], table, 6)
+    t.run(in_place=True)
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS
+    assert t.n_free.tolist() == [4] and t.free.tolist() == [2, 3, -1, 4, -7, -7] and (t.lens == 0).all()
+    t.new.zero_()
+    t.new[2] = 17
+    t.args = (17, 0)
+    t.pos, t.slots = (torch.full((17,), -9, dtype=torch.int64, device="cuda") for _ in range(2))
+    t.run(in_place=True)
+    torch.cuda.synchronize()
+    assert mg.maglev_device_status() == mg.MAGLEV_ERR_BOUNDS
+    assert t.slots.tolist() == list(range(64, 80)) + [-1] and t.pos.tolist() == list(range(16)) + [-1]
+    assert t.n_free.tolist() == [2] and t.free[:2].tolist() == [2, 3]
 
 
 def test_page_tables_without_token_rows():

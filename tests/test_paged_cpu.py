@@ -74,6 +74,15 @@ def test_page_tables_take_nothing_from_a_row_of_a_bad_length():
     assert got["free"] == [13, 5, 6, 7, 8] and got["seq_len"].tolist() == [0] * 3
 
 
+def test_page_tables_give_back_only_pages():
+    """Hand-worked: first columns without a page (negative: given back before) and rows whose length lies outside them put
+    nothing on the stack, another number outside the pool puts -1 there."""
+    table = np.array([[-1, -1, 5, 6], [-5, -1, -1, -1], [1, 30, -1, -1], [2, 3, 4, -1], [0, 10, 11, 12]])
+    got = oracle.page_tables([60, 64, 30, 65, -1], [-1] * 5, 0, 0, 16, [13], table, num_pages=30)
+    assert got["free"] == [13, 5, 6, 1, -1] and got["seq_len"].tolist() == [0] * 5
+    np.testing.assert_array_equal(got["block_table"], table)
+
+
 def _paged_from_forward(seed, T, H, hd, W, ps, inject):
     """A forward pass's entries of one sequence in scattered pages, and what went into it."""
     r = rng(seed)
