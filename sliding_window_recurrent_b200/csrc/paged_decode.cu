@@ -86,28 +86,22 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = upper part + rest: the upper 16 bits of x (x rounded to bf16 towards zero) and
-// what is left, rounded to nearest. Together they carry x to 2^-16. The rest has
-// x's sign and is never zero beside an x that is not: an infinite key or value
-// times both parts then is the infinity that it is times x, where inf * 0 or inf - inf
-// would be a NaN. (The smallest normal number in its place adds nothing otherwise.)
-__device__ __forceinline__ uint32_t upper2(float x, float y) {
-  return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+// x = upper part + rest: the largest bf16 number nearer to zero than x, and what is left
+// (at most one step of bf16), rounded to nearest. Together they carry x to 2^-16. Both
+// have x's sign, and the rest of an x that is not zero is not zero either: an infinite key
+// or value times both parts then is the infinity that it is times x, where inf * 0 or
+// inf - inf would be a NaN. Of a bf16 number the sum is exact, and zero stays zero.
+__device__ __forceinline__ uint32_t below(float x) {  // its upper 16 bits are the upper part's
+  const uint32_t u = __float_as_uint(x);
+  return u - ((u & 0x7fffffffu) != 0);
 }
+__device__ __forceinline__ uint32_t upper2(float x, float y) { return __byte_perm(below(x), below(y), 0x7632); }
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
   __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-__device__ __forceinline__ float rest(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-constexpr float TINY = 1.17549435e-38f;  // 2^-126
-__device__ __forceinline__ uint32_t rest2_weights(float x, float y) {  // x, y >= 0
-  return pack2(fmaxf(rest(x), TINY), fmaxf(rest(y), TINY));
-}
-__device__ __forceinline__ float rest_signed(float x) {
-  const float r = rest(x);
-  return r == 0.f && x != 0.f ? copysignf(TINY, x) : r;
-}
-__device__ __forceinline__ uint32_t rest2(float x, float y) { return pack2(rest_signed(x), rest_signed(y)); }
+__device__ __forceinline__ float rest(float x) { return x - __uint_as_float(below(x) & 0xffff0000u); }
+__device__ __forceinline__ uint32_t rest2(float x, float y) { return pack2(rest(x), rest(y)); }
 
 // A running reference may lie this far (log2 units) below the maximum before it
 // moves: weights stay below 2^8, and the rescaling of o becomes rare.
@@ -274,10 +268,10 @@ struct MmaTile {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (ONE) {
-          ph[n][e] = transpose8x8(lower ? rest2_weights(w[2 * e], w[2 * e + 1]) : upper2(w[2 * e], w[2 * e + 1]));
+          ph[n][e] = transpose8x8(lower ? rest2(w[2 * e], w[2 * e + 1]) : upper2(w[2 * e], w[2 * e + 1]));
         } else {
           ph[n][e] = transpose8x8(upper2(w[2 * e], w[2 * e + 1]));
-          pl[n][e] = transpose8x8(rest2_weights(w[2 * e], w[2 * e + 1]));
+          pl[n][e] = transpose8x8(rest2(w[2 * e], w[2 * e + 1]));
         }
       }
     }

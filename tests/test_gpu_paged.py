@@ -613,6 +613,44 @@ def test_decode_masked_garbage_and_infinities(dtype, H, H_kv):
     assert torch.equal(s.run(), without)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (4, 1), (8, 1), (16, 1)])
+@pytest.mark.parametrize("gap", [20, 60, 80, 85, 200, 1000])
+def test_decode_huge_values_behind_small_weights(dtype, H, H_kv, gap):
+    """A value near the type's largest with a weight of e^-gap contributes what the formula says, and nothing (the same
+    bits as a zero) where the weight lies below fp32's range. Every query is the same, and one key points against it.
+    The weight errs by a factor of at most 1 + 2 e + 2^-16 + (8 + n) U (see the file's head), the sum relative to the sum
+    of the terms' magnitudes, and the output by its rounding."""
+    s = Step(83, [60], H, H_kv, 128, 16, dtype=dtype)
+    s.q[:] = s.q[:, :1]
+    rot = oracle.rope(host(s.q)[:, :1], np.full((1, 1), 60), 10000.0)[0, 0]
+    page, row = int(s.table_h[0, 33 // 16]), 33 % 16
+    s.run()  # stores the new entry
+    torch.cuda.synchronize()
+
+    def rows(pool):
+        return host(pool)[s.table_h[0, np.arange(61) // 16], 0, np.arange(61) % 16]
+
+    scores = rows(s.kp) @ rot / np.sqrt(128)
+    top = np.max(np.delete(scores, 33))
+    s.kp[page, 0, row] = torch.from_numpy(rot * ((top - gap) * np.sqrt(128) / (rot @ rot))).to(TD[dtype])
+    s.vp[page, 0, row] = 0
+    without = s.run().clone()
+    s.vp[page, 0, row] = 3e38
+    got = s.run()
+    torch.cuda.synchronize()
+    if gap >= 200:
+        assert torch.equal(got, without)
+        return
+    keys, vals = rows(s.kp), rows(s.vp)
+    w = keys @ rot / np.sqrt(128)
+    w = np.exp(w - w.max())
+    w /= w.sum()
+    e = (2.0 ** -16 + 160 * U) * np.linalg.norm(rot) * np.linalg.norm(keys, axis=-1).max() / np.sqrt(128)
+    tol = HALF[dtype] * np.abs(w @ vals) + (2 * e + 2.0 ** -16 + (8 + 61) * U) * (w @ np.abs(vals))
+    within(host(got)[0], np.broadcast_to(w @ vals, (H, 128)), np.broadcast_to(tol, (H, 128)), f"gap {gap}")
+
+
 def test_decode_far_positions_and_large_scores():
     """Angles at positions near 2^24 (fp32 cannot hold them), and scores of some hundreds: the running maximum has
     to move, and most weights underflow."""
