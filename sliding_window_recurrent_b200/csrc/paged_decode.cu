@@ -512,8 +512,15 @@ __device__ __forceinline__ Sequence sequence_at(const PagedShape& s, const Decod
   return r;
 }
 
+// A position; EARLY: read before this kernel has waited for the last one. The kernel before has waited for whatever wrote
+// the positions, so they lie in L2, but only a wait of its own says that this SM's L1 holds nothing older.
+template <bool EARLY>
+__device__ __forceinline__ int64_t position(const DecodeArgs& a, int b) {
+  return EARLY ? (int64_t)__ldcg(reinterpret_cast<const long long*>(a.pos) + b) : a.pos[b];
+}
+template <bool EARLY = false>
 __device__ __forceinline__ Sequence sequence(const PagedShape& s, const DecodeArgs& a, int b) {
-  return sequence_at(s, a, a.pos[b]);
+  return sequence_at(s, a, position<EARLY>(a, b));
 }
 
 // The costs of all units in order make one line, which is cut into equal ranges.
@@ -530,7 +537,7 @@ struct Steps {
   int64_t total, per;  // cost of all units, of a team's range
   int chunk;
 };
-template <int THREADS, int TEAMS>
+template <bool EARLY, int THREADS, int TEAMS>
 __device__ __forceinline__ Steps form_plan(Plan<THREADS, TEAMS>& plan, const PagedShape& s, const DecodeArgs& a) {
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   Steps r;
@@ -540,7 +547,7 @@ __device__ __forceinline__ Steps form_plan(Plan<THREADS, TEAMS>& plan, const Pag
   for (int b = b0; b < b1; b += 8) {
     int64_t p[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = b + e < b1 ? a.pos[b + e] : -1;
+    for (int e = 0; e < 8; ++e) p[e] = b + e < b1 ? position<EARLY>(a, b + e) : -1;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mine += sequence_at(s, a, p[e]).cost;
   }
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
 
   wait_for_last();
   let_next_start();  // the join's blocks may take the places that come free
-  const Steps steps = form_plan(plan, s, a);
+  const Steps steps = form_plan<false>(plan, s, a);
   const int64_t per = steps.per, total = steps.total;
   const int me = blockIdx.x * TEAMS + team;
   const int64_t t0 = per * me, t1 = t0 + per < total ? t0 + per : total;  // the team's range
@@ -918,7 +925,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedSha
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = lane % V * 4;
   const int each = NW / per_block, rank = warp % each;  // warps of a head
   const int longest = 4 * FLY * SHARE * each;                               // parts they take alone: four loads' time
-  const Steps steps = form_plan(plan, s, a);  // reads nothing that the first kernel writes
+  const Steps steps = form_plan<true>(plan, s, a);  // reads nothing that the first kernel writes
   const int64_t heads = (int64_t)s.B * s.H, stride = (int64_t)2 * a.heads * PART_ROW;  // from team to team
   const int groups = a.units / s.Hkv, per_kv = s.H / s.Hkv;
   bool waited = false;
@@ -928,17 +935,17 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedSha
     Parts p{nullptr, nullptr, 1};
     if (mine) {
       const int b = (int)(head / s.H), h = (int)(head % s.H), hk = h / per_kv, in_kv = h - hk * per_kv;
-      const Sequence q = sequence(s, a, b);
+      const Sequence q = sequence<true>(s, a, b);
       const int i = b / steps.chunk;
       int64_t base = plan.before[i];
-      for (int x = i * steps.chunk; x < b; ++x) base += sequence(s, a, x).cost;
+      for (int x = i * steps.chunk; x < b; ++x) base += sequence<true>(s, a, x).cost;
       // the unit's first step, and the teams that have steps of it
       base = base * a.units + (int64_t)(hk * groups + in_kv / a.heads) * q.cost + UNIT_COST;
       const int w0 = (int)(base / steps.per);
       p.np = q.cost ? (int)((base + q.cost - UNIT_COST - 1) / steps.per) - w0 + 1 : 0;
       p.rest = a.parts + w0 * stride + in_kv % a.heads * PART_ROW;
       p.first = p.rest + (base > steps.per * w0 ? stride / 2 : 0);  // behind other units of team w0's range
-      if (p.np == 0 && rank == 0 && lane == 0 && a.pos[b] >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
+      if (p.np == 0 && rank == 0 && lane == 0 && position<true>(a, b) >= 0) record_error(a.err, DEV_BOUNDS);  // beyond the table
     }
     if (!waited) wait_for_last();  // the parts are written
     waited = true;

@@ -273,3 +273,16 @@ def test_dependent_kernels_promise_nothing_about_their_inputs():
             seen += 1
             assert "__restrict__" not in text and "__ldg(" not in text, os.path.basename(path)
     assert seen == 2
+
+
+def test_the_join_reads_positions_past_l1():
+    """What the join reads before it has waited for the first kernel is visible in L2 only (that kernel has waited for
+    whatever wrote it): every position it reads has to come from there."""
+    import os
+    import re
+    with open(os.path.join(_build.CSRC, "paged_decode.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    body = text[text.index("paged_join_kernel(PagedShape"):text.index("int units_of(")]
+    assert "wait_for_last()" in body and "a.pos[" not in body
+    reads = re.findall(r"\b(?:form_plan|sequence|position)\b(<\w+>)?\(", body)
+    assert len(reads) == 4 and set(reads) == {"<true>"}
