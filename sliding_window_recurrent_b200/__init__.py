@@ -141,16 +141,19 @@ def _ptr(x):
     return x.data_ptr()
 
 
-def _current_stream() -> int:
-    """Handle of torch's current stream on the current device. torch's own raw lookup: building a
-    torch.cuda.Stream object for it took 3 us of a 10 us call."""
-    global _current_stream
+def _stream_lookup():
+    """What gives the handle of torch's current stream on the current device: torch's own raw lookup where it has one
+    (building a torch.cuda.Stream object took 3 us of a 10 us call), else the public one."""
     import torch
-    raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+    raw, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+    if raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
-    def _current_stream() -> int:
-        return raw(device())
 
+def _current_stream() -> int:
+    global _current_stream
+    _current_stream = _stream_lookup()
     return _current_stream()
 
 

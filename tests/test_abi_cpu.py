@@ -168,3 +168,18 @@ def test_debug_build_exports_every_symbol():
     for n in mg.header_symbols():
         assert hasattr(lib, n), n
     assert mg.MAGLEV_ERR_BOUNDS == 5
+
+
+def test_current_stream_without_torchs_raw_lookup(monkeypatch):
+    """The raw lookup is no public name of torch: without it the calls take the public, slower one."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream = 4711
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert mg._stream_lookup()() == 4711
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 100 + device, raising=False)
+    assert mg._stream_lookup()() == 103
