@@ -115,11 +115,18 @@ def _paged_desc(tables, H, H_kv, hd, window, dtype, inject, rope_base, eps, shar
                      dtype=CODE[dtype], shared_kv_gates=int(shared_kv_gates))
 
 
-def _need(name, t, shape, dtype):
-    """A dense device tensor of this shape and type: the library sees its address only."""
-    if t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+def _need(name, t, shape, dtype, device):
+    """A dense tensor of this shape and type on the owner's GPU: the library sees its address only."""
+    if (t is None or tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or t.device != device
+            or not t.is_contiguous()):
         have = "None" if t is None else f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}"
-        raise ValueError(f"{name} must be a dense {shape} {dtype} tensor on the device, not {have}")
+        raise ValueError(f"{name} must be a dense {shape} {dtype} tensor on {device}, not {have}")
+
+
+def _need_current(device):
+    """The library launches on the current device, whatever its pointers belong to."""
+    if device.type == "cuda" and torch.cuda.current_device() != device.index:
+        raise ValueError(f"the buffers lie on {device}, which is not the current device")
 
 
 class PageTables:
@@ -138,6 +145,7 @@ class PageTables:
         self.free_pages = torch.arange(num_pages - 1, -1, -1, **i32)  # page 0 is handed out first
         self.n_free = torch.full((1,), num_pages, **i32)
         self.lengths = torch.zeros(B, **i64)
+        self.device = self.block_table.device
         self.cu_tokens = torch.zeros(B + 1, **i64)
         self.pos = torch.full((max_tokens,), -1, **i64)
         self.slots = torch.full((max_tokens,), -1, **i64)
@@ -151,7 +159,8 @@ class PageTables:
         n = self.max_tokens if n_tokens is None else n_tokens
         if n > self.max_tokens:
             raise ValueError(f"n_tokens {n} exceeds the {self.max_tokens} rows this table was made for")
-        _need("new_len", new_len, (self.B,), torch.int64)
+        _need_current(self.device)
+        _need("new_len", new_len, (self.B,), torch.int64, self.device)
         maglev_page_tables(self.desc, self.lengths, new_len, n, pad, self.free_pages, self.n_free, self.block_table,
                            self.lengths, self.n_free, self.cu_tokens, self.pos, self.slots, self.workspace, stream)
         return self.pos[:n], self.slots[:n]
@@ -171,6 +180,9 @@ class PagedLayerState:
         self.k_pages = torch.empty(tables.num_pages, H_kv, tables.page_size, hd, dtype=td, device=device)
         self.v_pages = torch.empty_like(self.k_pages)
         self.out = torch.empty(B, H, hd, dtype=td, device=device)
+        self.device = self.out.device
+        if self.device != tables.device:
+            raise ValueError(f"the layer's pages would lie on {self.device}, its tables lie on {tables.device}")
         self.krec = torch.empty(B, H_kv, hd, dtype=td, device=device) if inject else None
         self.vrec = torch.empty(B, H_kv, hd, dtype=td, device=device) if inject else None
         self.mem_desc = DecodeDesc(B=B, H=H_kv, hd=hd, d_mem=d_mem, window=1, rope_base=rope_base, rms_eps=eps,
@@ -181,11 +193,12 @@ class PagedLayerState:
     def write(self, slots, pos, k, v, R_k=None, R_v=None, gates=None, stream=None):
         """Entries of the token rows k, v [n, H_kv, hd] into their slots (pos None: as they are)."""
         n, rows = slots.numel(), (slots.numel(), self.desc.H_kv, self.desc.hd)
-        _need("slots", slots, (n,), torch.int64)
+        _need_current(self.device)
+        _need("slots", slots, (n,), torch.int64, self.device)
         if pos is not None:
-            _need("pos", pos, (n,), torch.int64)
+            _need("pos", pos, (n,), torch.int64, self.device)
         for name, t in (("k", k), ("v", v)) + ((("R_k", R_k), ("R_v", R_v)) if self.inject else ()):
-            _need(name, t, rows, self.dtype)
+            _need(name, t, rows, self.dtype, self.device)
         if self.inject:
             self._need_gates(gates)
         maglev_paged_write(self.desc, slots.numel(), slots, pos, k, v, R_k, R_v, gates, self.k_pages, self.v_pages,
@@ -195,15 +208,16 @@ class PagedLayerState:
         maglev_decode_mem_project(self.mem_desc, pos, m_prev, w_mk, w_mv, self.krec, self.vrec, stream)
 
     def _need_gates(self, gates):
-        _need("gates", gates, (2 if self.desc.shared_kv_gates else 4, self.desc.H_kv), torch.float32)
+        _need("gates", gates, (2 if self.desc.shared_kv_gates else 4, self.desc.H_kv), torch.float32, self.device)
 
     def step(self, pos, q, k, v, gates=None, stream=None):
         """Attention of one token per sequence, q [B, H, hd], k, v [B, H_kv, hd] at pos [B] (-1: not running)."""
         d = self.desc
-        _need("pos", pos, (d.B,), torch.int64)
-        _need("q", q, (d.B, d.H, d.hd), self.dtype)
-        _need("k", k, (d.B, d.H_kv, d.hd), self.dtype)
-        _need("v", v, (d.B, d.H_kv, d.hd), self.dtype)
+        _need_current(self.device)
+        _need("pos", pos, (d.B,), torch.int64, self.device)
+        _need("q", q, (d.B, d.H, d.hd), self.dtype, self.device)
+        _need("k", k, (d.B, d.H_kv, d.hd), self.dtype, self.device)
+        _need("v", v, (d.B, d.H_kv, d.hd), self.dtype, self.device)
         if self.inject:
             self._need_gates(gates)
         maglev_paged_decode_step(self.desc, pos, q, k, v, self.krec, self.vrec, gates, self.tables.block_table,

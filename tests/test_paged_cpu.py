@@ -286,3 +286,73 @@ def test_the_join_reads_positions_past_l1():
     assert "wait_for_last()" in body and "a.pos[" not in body
     reads = re.findall(r"\b(?:form_plan|sequence|position)\b(<\w+>)?\(", body)
     assert len(reads) == 4 and set(reads) == {"<true>"}
+
+
+# ---------------------------------------------------------------------------
+# the owner classes, with stand-ins for device tensors
+# ---------------------------------------------------------------------------
+class Placed:
+    """What the owners look at of a dense tensor on a GPU; it has no memory."""
+
+    def __init__(self, shape, dtype, index=0):
+        import torch
+        self.shape, self.dtype, self.device, self.is_cuda = shape, dtype, torch.device("cuda", index), True
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def stride(self):
+        return ()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        raise AssertionError("passed to the library")
+
+
+@pytest.fixture
+def owners(monkeypatch):
+    """A table and a layer whose (host) buffers are taken for ones on cuda:0, the current device."""
+    torch = pytest.importorskip("torch")
+    from sliding_window_recurrent_b200.layer import PagedLayerState, PageTables
+    T = PageTables(2, 16, 4, 8, 32, device="cpu")
+    L = PagedLayerState(T, 4, 64, 2, d_mem=16, inject=True, device="cpu")
+    T.device = L.device = torch.device("cuda", 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return torch, T, L
+
+
+def paged_arguments(torch):
+    i64, bf = torch.int64, torch.bfloat16
+    return (dict(new_len=((2,), i64)),
+            dict(slots=((2,), i64), pos=((2,), i64), k=((2, 2, 64), bf), v=((2, 2, 64), bf), R_k=((2, 2, 64), bf),
+                 R_v=((2, 2, 64), bf), gates=((4, 2), torch.float32)),
+            dict(pos=((2,), i64), q=((2, 4, 64), bf), k=((2, 2, 64), bf), v=((2, 2, 64), bf), gates=((4, 2), torch.float32)))
+
+
+@pytest.mark.parametrize("call", [0, 1, 2])
+def test_owners_refuse_tensors_on_another_device(owners, call):
+    """Each argument in turn on a second GPU: its address means nothing to a kernel on the first."""
+    torch, T, L = owners
+    fn = (T.step, L.write, L.step)[call]
+    spec = paged_arguments(torch)[call]
+    for name in spec:
+        with pytest.raises(ValueError, match=f"{name} must.*cuda:0"):
+            fn(**{n: Placed(*x, index=int(n == name)) for n, x in spec.items()})
+
+
+def test_owners_refuse_another_current_device(owners, monkeypatch):
+    """The library launches on the current device: its owners' buffers have to lie there."""
+    torch, T, L = owners
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for fn, spec in zip((T.step, L.write, L.step), paged_arguments(torch)):
+        with pytest.raises(ValueError, match="not the current device"):
+            fn(**{n: Placed(*x) for n, x in spec.items()})
+
+
+def test_a_layer_lies_where_its_tables_do(owners):
+    torch, T, _ = owners
+    from sliding_window_recurrent_b200.layer import PagedLayerState
+    with pytest.raises(ValueError, match="its tables lie on cuda:0"):
+        PagedLayerState(T, 4, 64, 2, device="cpu")
