@@ -205,6 +205,13 @@ class PagedLayerState:
                            stream)
 
     def mem_project(self, pos, m_prev, w_mk, w_mv, stream=None):
+        """The step's memory entries (inject): m_prev [B, d_mem], w_mk, w_mv [H_kv * hd, d_mem]."""
+        d, weights = self.mem_desc, (self.desc.H_kv * self.desc.hd, self.mem_desc.d_mem)
+        _need_current(self.device)
+        _need("pos", pos, (d.B,), torch.int64, self.device)
+        _need("m_prev", m_prev, (d.B, d.d_mem), self.dtype, self.device)
+        _need("w_mk", w_mk, weights, self.dtype, self.device)
+        _need("w_mv", w_mv, weights, self.dtype, self.device)
         maglev_decode_mem_project(self.mem_desc, pos, m_prev, w_mk, w_mv, self.krec, self.vrec, stream)
 
     def _need_gates(self, gates):

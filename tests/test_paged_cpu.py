@@ -356,3 +356,14 @@ def test_a_layer_lies_where_its_tables_do(owners):
     from sliding_window_recurrent_b200.layer import PagedLayerState
     with pytest.raises(ValueError, match="its tables lie on cuda:0"):
         PagedLayerState(T, 4, 64, 2, device="cpu")
+
+
+def test_mem_project_refuses_what_the_library_would_misread(owners):
+    """Each argument too small, of another type and on another device: the library would read past its end."""
+    torch, T, L = owners
+    bf = torch.bfloat16
+    good = dict(pos=((2,), torch.int64), m_prev=((2, 16), bf), w_mk=((128, 16), bf), w_mv=((128, 16), bf))
+    for name, (shape, dtype) in good.items():
+        for bad in (Placed((shape[0] - 1,) + shape[1:], dtype), Placed(shape, torch.float32), Placed(shape, dtype, 1), None):
+            with pytest.raises(ValueError, match=f"{name} must"):
+                L.mem_project(**{**{n: Placed(*x) for n, x in good.items()}, name: bad})
