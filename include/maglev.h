@@ -146,7 +146,9 @@ maglev_status maglev_device_status(void* stream, int* code);
 maglev_status maglev_wait_selftest(const void* src, int bytes, int64_t spin_limit, void* stream);
 
 /* Bytes of the activations the forward saves for the backward ("saved"):
- * the rotated queries and the mixed keys/values, 3 x [B,T,H,hd] of dtype. */
+ * the rotated queries and the mixed keys/values, q_rot, k_bar, v_bar, each a
+ * dense [B,T,H,hd] of dtype that begins at a multiple of 256 bytes: at 0, n and
+ * 2n, with n = a third of the size. */
 size_t maglev_swa_saved_bytes(const maglev_swa_desc* desc);
 
 /* Bytes of scratch memory maglev_inject_swa_bwd needs ("workspace"). */
@@ -477,8 +479,8 @@ size_t maglev_page_tables_workspace_bytes(const maglev_paged_desc* desc);
  *   pos [n] int64: absolute positions; then k_bar = RoPE_pos(k), v_bar = v, and with
  *     desc->inject k_bar = g_kl RoPE_pos(k) + g_kr RoPE_pos(RMSNorm_head(R_k)),
  *     v_bar = g_vl v + g_vr R_v ([rainbus] 方法步骤详情). NULL: k and v already are entries
- *     (rows of the forward's `saved` k_bar, v_bar) and are stored as they are;
- *     desc->inject must be 0.
+ *     (rows of the forward's `saved` k_bar, v_bar; maglev_swa_saved_bytes tells
+ *     where they lie) and are stored as they are; desc->inject must be 0.
  *   k, v, R_k, R_v [n, H_kv, hd] (R_k, R_v, gate_logits: only with inject);
  *     k_pages, v_pages (in/out): no other slot changes.
  * Uses neither block_table nor desc's B, H, max_pages and window. n == 0 enqueues

@@ -22,6 +22,14 @@ def _bytes(n: int, device) -> torch.Tensor:
     return torch.empty(max(int(n), 16), dtype=torch.uint8, device=device)
 
 
+def saved_entries(desc, saved):
+    """The mixed keys and values k_bar, v_bar [B, T, H, hd] in a forward's `saved` buffer, as views of it."""
+    shape, third = (desc.B, desc.T, desc.H, desc.hd), maglev_swa_saved_bytes(desc) // 3
+    td = torch.bfloat16 if desc.dtype == MAGLEV_BF16 else torch.float32
+    size = desc.B * desc.T * desc.H * desc.hd * td.itemsize
+    return tuple(saved[i * third:i * third + size].view(td).view(shape) for i in (1, 2))
+
+
 class InjectedSWALayer:
     def __init__(self, B, T, H, hd, d_mem, window, dtype="bf16", inject=True, pos0=0,
                  rope_base=10000.0, eps=1e-6, device="cuda", spin_limit=0, shared_kv_gates=False):
@@ -57,6 +65,11 @@ class InjectedSWALayer:
         maglev_inject_swa_fwd(self.desc, q, k, v, m_shift if self.inject else None, w_mk, w_mv,
                               self.R_k, self.R_v, gates, self.out, self.lse, self.saved, stream)
         return self.out
+
+    def entries(self):
+        """The last forward's mixed keys and values [B, T, H, hd], views of `saved`: what a paged cache stores of a prompt
+        (PagedLayerState.write without positions, rows b * T + t)."""
+        return saved_entries(self.desc, self.saved)
 
     def consistency(self, m, target, lam, dm=None, accumulate_dm=False, inv_count=0.0, stream=None):
         rows = m.numel() // m.shape[-1]
@@ -174,6 +187,7 @@ class PagedLayerState:
         self.tables = tables
         H_kv = H if H_kv is None else H_kv
         self.desc = _paged_desc(tables, H, H_kv, hd, window, dtype, inject, rope_base, eps, shared_kv_gates)
+        self.copy_desc = _paged_desc(tables, H, H_kv, hd, window, dtype, False, rope_base, eps, shared_kv_gates)
         td = TORCH_DTYPE[dtype]
         B = tables.B
         self.dtype, self.inject = td, bool(inject)
@@ -191,18 +205,19 @@ class PagedLayerState:
         self.workspace = _bytes(maglev_paged_decode_workspace_bytes(self.desc), device)
 
     def write(self, slots, pos, k, v, R_k=None, R_v=None, gates=None, stream=None):
-        """Entries of the token rows k, v [n, H_kv, hd] into their slots (pos None: as they are)."""
+        """Entries of the token rows k, v [n, H_kv, hd] into their slots. pos None: k and v are entries that a forward has
+        mixed and are stored as they are, in an injected layer too (R_k, R_v and gates then are not used)."""
         n, rows = slots.numel(), (slots.numel(), self.desc.H_kv, self.desc.hd)
+        desc, inject = (self.copy_desc, False) if pos is None else (self.desc, self.inject)
         _need_current(self.device)
         _need("slots", slots, (n,), torch.int64, self.device)
         if pos is not None:
             _need("pos", pos, (n,), torch.int64, self.device)
-        for name, t in (("k", k), ("v", v)) + ((("R_k", R_k), ("R_v", R_v)) if self.inject else ()):
+        for name, t in (("k", k), ("v", v)) + ((("R_k", R_k), ("R_v", R_v)) if inject else ()):
             _need(name, t, rows, self.dtype, self.device)
-        if self.inject:
+        if inject:
             self._need_gates(gates)
-        maglev_paged_write(self.desc, slots.numel(), slots, pos, k, v, R_k, R_v, gates, self.k_pages, self.v_pages,
-                           stream)
+        maglev_paged_write(desc, n, slots, pos, k, v, R_k, R_v, gates, self.k_pages, self.v_pages, stream)
 
     def mem_project(self, pos, m_prev, w_mk, w_mv, stream=None):
         """The step's memory entries (inject): m_prev [B, d_mem], w_mk, w_mv [H_kv * hd, d_mem]."""

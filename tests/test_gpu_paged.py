@@ -996,6 +996,52 @@ def test_serving_run(dtype, H, H_kv, window, inject):
     assert refused < 14 * B
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inject", [False, True])
+@pytest.mark.parametrize("B,T,H,hd,W", [(1, 77, 1, 64, 32), (2, 45, 3, 128, 20), (3, 128, 10, 128, 512)])
+def test_a_prompts_entries_move_from_the_forward_to_pages(dtype, inject, B, T, H, hd, W):
+    """The forward of the dense layer, its entries (also where a third of `saved` is padded to 256 bytes) as they are into
+    pages, and a step behind them: the entries against the oracle's, the pages bit for bit, the step against the oracle
+    over the pages as they are."""
+    from sliding_window_recurrent_b200.layer import InjectedSWALayer
+    d_mem, ps, gen = 64, 16, generator(T)
+    F = InjectedSWALayer(B, T, H, hd, d_mem, W, dtype, inject)
+    q, k, v = (normal(gen, (B, T, H, hd), dtype) for _ in range(3))
+    gates = torch.rand(4, H, generator=gen, device="cuda") * 4 - 2 if inject else None
+    m = normal(gen, (B, T, d_mem), dtype)
+    w_mk, w_mv = (normal(gen, (H * hd, d_mem), dtype) / 8 for _ in range(2))
+    F.forward(q, k, v, gates, m if inject else None, w_mk, w_mv)
+    kb, vb = F.entries()
+    assert kb.shape == vb.shape == (B, T, H, hd) and kb.data_ptr() % 256 == vb.data_ptr() % 256 == F.saved.data_ptr() % 256
+    torch.cuda.synchronize()
+    for b in range(B):
+        Rk, Rv = (host(x)[b].reshape(T, H, hd) if inject else None for x in (F.R_k, F.R_v))
+        g = host(gates) if inject else None
+        ref_k, ref_v = oracle.paged_entries(np.arange(T), host(k)[b], host(v)[b], Rk, Rv, g)
+        tk, tv = entry_bound(None, host(k)[b], host(v)[b], Rk, Rv, g, ref_k, ref_v, dtype)
+        within(host(kb)[b], ref_k, tk, "k_bar")
+        within(host(vb)[b], ref_v, tv, "v_bar")
+    tabs = PageTables(B, ps, -(-T // ps) + 1, B * (-(-T // ps) + 1), B * T)
+    L = PagedLayerState(tabs, H, hd, H, W, d_mem, dtype, inject)
+    pos, slots = tabs.step(torch.full((B,), T, device="cuda"), B * T, T)
+    L.write(slots, None, kb.reshape(B * T, H, hd), vb.reshape(B * T, H, hd))
+    page, row = slots // ps, slots % ps
+    assert torch.equal(L.k_pages[page, :, row], kb.reshape(B * T, H, hd))
+    assert torch.equal(L.v_pages[page, :, row], vb.reshape(B * T, H, hd))
+    pos, _ = tabs.step(torch.ones(B, dtype=torch.int64, device="cuda"), B, 1)
+    if inject:
+        L.mem_project(pos, m[:, 0].contiguous(), w_mk, w_mv)
+    L.step(pos, q[:, 0].contiguous(), k[:, 0].contiguous(), v[:, 0].contiguous(), gates)
+    torch.cuda.synchronize()
+    kp, vp, table = host(L.k_pages), host(L.v_pages), tabs.block_table.cpu().numpy()
+    ref = oracle.paged_attention([T] * B, host(q)[:, 0], table, kp, vp, W)
+    j = np.arange(max(0, T - W + 1), T + 1)
+    keys, vals = (np.stack([x[table[b, j // ps], :, j % ps] for b in range(B)]) for x in (kp, vp))
+    e = (2.0 ** -16 + (hd + 32) * U) * np.linalg.norm(host(q)[:, 0], axis=-1).max() * np.linalg.norm(keys, axis=-1).max() / np.sqrt(hd)
+    within(host(L.out), ref, HALF[dtype] * np.abs(ref) + (2 * e + 2.0 ** -16 + (8 + len(j)) * U) * np.abs(vals).max(), "out")
+    assert mg.maglev_device_status() == 0
+
+
 def test_step_captured_in_a_graph_runs_on():
     """A whole serving step (tables in place, two layers) in one graph: replays continue the sequences by a token each,
     as separate calls do."""
