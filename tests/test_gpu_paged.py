@@ -499,6 +499,53 @@ def test_decode_windows(dtype, window, ps):
                      dtype=dtype))
 
 
+def in_two_parts(x):
+    """x as two bf16 numbers carry it: what a path on bf16 tensor cores would compute with."""
+    upper = torch.from_numpy(x).to(torch.bfloat16).double()
+    return (upper + (torch.from_numpy(x) - upper).to(torch.bfloat16).double()).numpy()
+
+
+@pytest.mark.parametrize("H,H_kv,hd", [(2, 2, 128), (4, 1, 64), (8, 1, 128), (12, 1, 64), (32, 2, 128)])
+def test_decode_keeps_fp32(H, H_kv, hd):
+    """fp32 to fp32's accuracy, with a bound that two bf16 parts (2^-16) do not keep to. Queries and keys live in the channel
+    that turns slowest, so that a score is one product and its error small: the turned query errs by 4 U (cosine and sine
+    of an angle below 2^-7, one rounding each), product, scale and the difference to the maximum by another 4 U, so the
+    score by e = 8 U of the largest one. A weight errs by e and 8 U of its power, two sums over n keys by n U each,
+    three parts' rescaling and joining by at most 8 factors of 5 U in each of the two sums: 2 e + (2 n + 96) U of the sum
+    of the terms' magnitudes, and the output by its rounding. The same sums with queries and keys in two parts lie outside."""
+    pos = np.array([0, 1, 15, 16, 31, 40, 39, 7])
+    s = Step(91, pos, H, H_kv, hd, 16, dtype="f32")
+    r = np.random.Generator(np.random.Philox(hd))
+    c = hd // 2 - 1
+    s.q.zero_()
+    s.q[:, :, c] = torch.from_numpy(r.standard_normal((len(pos), H)) * 30).float()
+    s.k.zero_()
+    s.k[:, :, c] = torch.from_numpy(r.standard_normal((len(pos), H_kv)) * 3).float()
+    s.kp[:] = s.kp * (torch.arange(hd, device="cuda") == c) * 3  # (NaN stays where nothing is read)
+    s.run()
+    torch.cuda.synchronize()
+    got, kp, vp = host(s.out), host(s.kp), host(s.vp)
+    rejected = False
+    for b, p in enumerate(pos):
+        q = oracle.rope(host(s.q)[b:b + 1], np.full((1, H), p), 10000.0)[0]
+        j = np.arange(p + 1)
+        keys, vals = (np.repeat(x[s.table_h[b, j // 16], :, j % 16], H // H_kv, 1) for x in (kp, vp))
+
+        def attend(q, keys):
+            x = np.einsum("hd,jhd->hj", q, keys) / np.sqrt(hd)
+            w = np.exp(x - x.max(1, keepdims=True))
+            return x, w / w.sum(1, keepdims=True)
+
+        x, w = attend(q, keys)
+        ref, mass = np.einsum("hj,jhd->hd", w, vals), np.einsum("hj,jhd->hd", w, np.abs(vals))
+        delta = 2 * 8 * U * np.abs(x).max(1, keepdims=True) + (2 * len(j) + 96) * U
+        tol = U * np.abs(ref) + delta * mass
+        within(got[b], ref, tol, f"sequence {b}")
+        worse = np.einsum("hj,jhd->hd", attend(in_two_parts(q), in_two_parts(keys))[1], vals)
+        rejected |= bool((np.abs(worse - ref) > tol).any())
+    assert rejected
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("window", [2**31 - 17, 2**31 - 16, 2**31 - 1])
 def test_decode_window_without_a_limit(dtype, window):
