@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(NW * 32, OCC) paged_decode_kernel(PagedShape s
     if (whole) {
       T* d = out + ((int64_t)cur.b * s.H + first) * HD;
       tile.each_out(
-          heads, [](float l) { return l == 0.f ? 0.f : 1.f / l; },
+          heads, [](float l) { return 1.f / l; },  // (no weight at all: 0 * inf, as the formula has it)
           [&](int j, int c, float x) { d[j * HD + c] = from_f<T>(x); });
     } else {
       // the unit that holds the range's first place, or the one that goes on behind its last
@@ -986,7 +986,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, 2) paged_join_kernel(PagedSha
     }
     if (!mine || p.np == 1 || rank != 0 || lane >= V) continue;  // np == 1: its team has written it
     T* out = static_cast<T*>(a.out) + head * HD;
-    const float f = r.l == 0.f ? 0.f : 1.f / r.l;
+    const float f = p.np == 0 ? 0.f : 1.f / r.l;
     out[c] = from_f<T>(r.o.x * f);
     out[c + 1] = from_f<T>(r.o.y * f);
     out[c + 2] = from_f<T>(r.o.z * f);

@@ -661,6 +661,33 @@ def test_decode_masked_garbage_and_infinities(dtype, H, H_kv):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (12, 1), (32, 1)])
+@pytest.mark.parametrize("window", [1, 40, 3000])
+def test_decode_without_any_weight_is_not_a_number(dtype, H, H_kv, window):
+    """Scores that are all minus infinity have no softmax: NaN, as in the formula, from one part or from several; zeros are
+    for sequences that do not run."""
+    pos = [2999, -1, 50]
+    s = Step(84, pos, H, H_kv, 128, 16, window=window, dtype=dtype)
+    s.q[:] = s.q[:, :1]
+    good = s.run().clone()
+    q = oracle.rope(host(s.q)[:1, :1], np.full((1, 1), 2999), 10000.0)[0, 0]
+    c = 5
+    lo = max(0, 2999 - window + 1)
+    j = np.arange(lo, 2999)
+    pages = s.table_h[0, j // 16]
+    s.kp[pages, :, j % 16, c] = float("-inf") if q[c] > 0 else float("inf")
+    # the new key is turned, which makes both channels of the pair infinite: of four ways one points away from q in both
+    turn = oracle.rope(np.eye(128)[None, [c, c + 64]], np.full((1, 2), 2999), 10000.0)[0][:, [c, c + 64]]
+    i, sign = next((i, z) for i in (0, 1) for z in (1, -1) if (z * turn[i] * q[[c, c + 64]] < 0).all())
+    s.k[0, :, c + 64 * i] = float("inf") * sign
+    out = s.run()
+    torch.cuda.synchronize()
+    new = host(s.kp)[s.table_h[0, 2999 // 16], 0, 2999 % 16][[c, c + 64]]
+    assert np.isinf(new).all() and (new * q[[c, c + 64]] < 0).all()
+    assert out[0].isnan().all() and (out[1] == 0).all() and torch.equal(out[2], good[2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("H,H_kv", [(1, 1), (4, 1), (8, 1), (16, 1)])
 @pytest.mark.parametrize("gap", [20, 60, 80, 85, 200, 1000])
 def test_decode_huge_values_behind_small_weights(dtype, H, H_kv, gap):
