@@ -433,7 +433,10 @@ size_t maglev_decode_workspace_bytes(const maglev_decode_desc* desc);
  *     It is served if its row has columns for them, its token rows exist (below)
  *     and the pages it needs are there: requests are taken in order, and one
  *     that needs pages is served only while the pages asked for by it and the
- *     requests before it fit into the free ones. A served request gets its
+ *     requests before it fit into the free ones. One that is refused for want of
+ *     pages still counts: behind it only requests that need none are served,
+ *     so running sequences belong in lower rows than waiting prompts, or the
+ *     prompt waits with new_len 0. A served request gets its
  *     new pages from the top of the free stack (columns in order) and the
  *     length ctx_len + new_len; another keeps its length and row.
  *   new_len[b] < 0: it is finished. Its pages go back on the free stack (in
@@ -444,6 +447,10 @@ size_t maglev_decode_workspace_bytes(const maglev_decode_desc* desc);
  *     Another number outside the pool is recorded as MAGLEV_ERR_BOUNDS, and -1
  *     takes its place on the stack (handed out, it gives no slots and is
  *     recorded again). A row whose length lies outside it gives nothing back.
+ *   Pages have no count of holders: those that the rows hold and those on the
+ *     stack have to differ from one another, or a page is handed out twice. Where
+ *     sequences share first pages, a row that finishes before the last holder has
+ *     those columns set to -1 first.
  *   A ctx_len below 0 or above max_pages * page_size is recorded as
  *     MAGLEV_ERR_BOUNDS whatever new_len is; such a request is not served.
  *   n_tokens, pad: token rows. pad == 0: packed, token i of request b is row
@@ -503,6 +510,7 @@ maglev_status maglev_paged_write(const maglev_paged_desc* desc, int64_t n, const
  *     stored. Columns of block_table outside those positions are not read, and
  *     neither is a page's content outside them. Entries whose page number lies
  *     outside the pool take no part (the new one still does, and is not stored).
+ *     Scores that are all minus infinity give NaN, like the formula.
  *     The pages that new entries are written to belong to one sequence each;
  *     others may be shared.
  *   out [B,H,hd] (out).

@@ -27,17 +27,18 @@
 // 109 at 64 ragged sequences, 103 to 113 against 99 at 8 long ones.)
 //
 // Measured (one B200, GPU time in a graph; share of the bytes' time at 6535 GB/s):
-//   64 sequences of 64..4096, 10 heads of 128, bf16          109.5 us  0.95
+//   64 sequences of 64..4096, 10 heads of 128, bf16          109.6 us  0.95
 //   8 of 8192..65536, 32 query heads on 4 of 128, bf16        98.6 us  0.94
-//   64 of 128..8192, window 512, 10 of 128, bf16              34.3 us  0.74
+//   64 of 128..8192, window 512, 10 of 128, bf16              34.7 us  0.73
 //   2 of 15005, 30010, 8 on 4 heads of 64, fp32               24.1 us  0.58
-//   1 of 190, 10 of 128, bf16                                  7.4 us  (latency)
+//   1 of 190, 10 of 128, bf16                                  7.6 us  (latency)
 // Beside the streaming each call pays about 3.5 us from the launch to the first data
 // (positions, page numbers and entries are three loads that depend on one another),
 // 2 us for the join, and what the slowest SM takes longer than the average (3 to 8 us).
 // More than 8 (fp32: 4) query heads to a key/value head are shared by a team of two or
 // four warps, each with its own heads, over one ring of stages: the cache is read
-// once for up to 32 (16) heads. Their arithmetic then is what binds: 0.76 of the
+// once for up to 32 (16) heads. Heads come in eights (fours): with 9 to 15, or 17 to 24,
+// a warp of the team has little to do. Their arithmetic then is what binds: 0.76 of the
 // bytes' time at 16 heads of 128, 0.43 at 24, 0.66 at 8 in fp32 (0.72, 0.42, 0.45 with
 // wider tiles or several passes).
 // Eight warps with two 8 KB stages each (128 KB in flight on an SM) are what HBM
@@ -119,8 +120,10 @@ __device__ __forceinline__ uint32_t piece(int r, int c) {
 // take the keys (the channels) as the instruction's 16 rows and the heads as its
 // columns: with one head to a key head the heads are the side to pad, and 8
 // columns is the least it can be padded to. The step is bound by HBM (8 KB per 16
-// keys), which leaves room to carry q and P as two bf16 parts each: S and O then are
-// fp32-accurate and the only rounding is the output's. The 8 NT columns hold
+// keys, up to 8 heads), which leaves room to carry q and P as two bf16 parts each, that
+// is to 2^-16: a score errs by up to 2^-16 |q| |k| / sqrt(hd), a weight by that and 2^-16
+// of itself. For scores of some tens that is far below the output's rounding (2^-8); it
+// reaches it where |q| |k| / sqrt(hd) is some hundreds. The 8 NT columns hold
 // both parts: up to 4 heads in one tile (columns 0-3 the upper, 4-7 the lower
 // parts), 8 heads in two (the upper parts in the first).
 // ---------------------------------------------------------------------------

@@ -23,8 +23,8 @@ namespace {
 // plan (one block: prefix sums over the requests) takes one barrier a sum, the
 // fill (a thread per token row) finds its requests by block-wide counts instead of a
 // chain of probes, and is scheduled while the plan runs. Up to ONE_LAUNCH_ROWS rows
-// the plan's block does the rows itself. GPU time: 64 single tokens 3.2 us, 96
-// prompts and ends (74 k rows) 6.0 us, 2048 requests (52 k rows) 10.6 us.
+// the plan's block does the rows itself. GPU time: 64 single tokens 3.3 us, 96
+// prompts and ends (74 k rows) 6.2 us, 2048 requests (52 k rows) 10.7 us.
 // ---------------------------------------------------------------------------
 struct PlanTotals {
   int64_t n_old, avail, left;  // free pages before, with the returned ones, after
@@ -366,9 +366,10 @@ __global__ void __launch_bounds__(FILL_ROWS) page_fill_kernel(PageTablesArgs a, 
 // at a time; hd/16 threads cover a row and reduce its RMS with shuffles. A thread
 // keeps its head (and gates) and goes through the block's tokens, `pass` of them
 // at a time; their angles (double products, shared by the heads) are formed once
-// into shared memory while the first loads are on their way. Bound by HBM: 65536
-// rotated rows of 10 x 128 bf16 take 106 us (0.95 of the copy rate), 8192 mixed ones
-// 26 us (0.73: about three waves of blocks), 64 rows 2.8 us.
+// into shared memory while the first loads are on their way. Bound by HBM, of 10 x 128:
+// 65536 rotated rows in bf16 take 107 us (0.94 of the copy rate), 32768 in fp32 106
+// (0.95); mixed ones in bf16 83 us for 32768 (0.91) and 26 for 8192 (0.73: about three
+// waves of blocks), in fp32 158 (0.95) and 45 (0.85); 64 rows 2.8 us.
 // ---------------------------------------------------------------------------
 enum { WRITE_COPY = 0, WRITE_ROPE = 1, WRITE_MIX = 2 };
 constexpr int WRITE_THREADS = 256;
@@ -513,7 +514,9 @@ cudaError_t write_pages(const PagedShape& s, int64_t n, const int64_t* slots, co
   constexpr int ROWS = WRITE_THREADS / (HD / 16), MOST = WRITE_TURNS / (HD / 2);
   const int heads = s.Hkv < ROWS ? s.Hkv : ROWS, pass = ROWS / heads;  // of a block; tokens at a time
   // two passes a block: one leaves the angles uncovered, four leave a ragged last wave
-  // (8192 mixed rows of 10 x 128 bf16: 27.3, 26.2, 27.8 us with 1, 2, 4 passes)
+  // (10 x 128 with 1, 2, 4 passes: 8192 mixed rows in bf16 26.9, 25.9, 27.0 us, 16384 48.4,
+  // 45.0, 47.1, in fp32 85.6, 83.5, 82.2; 65536 rotated in bf16 114.4, 107.8, 106.9, 4096
+  // 9.5, 10.2, 10.2)
   int tile = pass * 2 < MOST ? pass * 2 : MOST;
   while (tile > 1 && n < (int64_t)tile * 4 * num_sms()) tile /= 2;  // few tokens: spread them over the SMs
   const dim3 blocks((unsigned)((n + tile - 1) / tile), (unsigned)((s.Hkv + heads - 1) / heads));

@@ -168,7 +168,8 @@ class PageTables:
 
     def step(self, new_len, n_tokens=None, pad=0, stream=None):
         """new_len [B] int64 on the device: tokens each sequence brings, -1 where it is finished.
-        Returns (pos, slots) of the first n_tokens rows (packed; pad > 0: row b * pad + i)."""
+        Returns (pos, slots) of the first n_tokens rows (packed; pad > 0: row b * pad + i), views that the next step
+        writes over."""
         n = self.max_tokens if n_tokens is None else n_tokens
         if n > self.max_tokens:
             raise ValueError(f"n_tokens {n} exceeds the {self.max_tokens} rows this table was made for")

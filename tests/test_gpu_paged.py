@@ -1116,6 +1116,64 @@ def test_a_prompts_entries_move_from_the_forward_to_pages(dtype, inject, B, T, H
     assert mg.maglev_device_status() == 0
 
 
+def test_pages_behind_a_window_and_shared_ones_are_given_back_once():
+    """What the tables leave to the caller: pages that a window has passed go on the stack and their columns to -1, and a
+    row that shares its first pages finishes with those columns at -1. Outputs are those of a cache that keeps every page,
+    each page is on the stack or in one row's columns at any time, and at the end all are back."""
+    B, H, hd, ps, W, pool = 3, 2, 64, 16, 20, 30
+    gen = generator(95)
+    one = torch.ones(B, dtype=torch.int64, device="cuda")
+    caches = []
+    for _ in range(2):
+        T = PageTables(B, ps, 16, pool, 128)
+        L = PagedLayerState(T, H, hd, window=W)
+        caches.append((T, L))
+    k0, v0 = normal(gen, (128, H, hd), "bf16"), normal(gen, (128, H, hd), "bf16")
+    for T, L in caches:
+        pos, slots = T.step(torch.tensor([40, 5, 0], device="cuda"), 45)
+        L.write(slots, pos, k0[:45], v0[:45])
+    # the third sequence continues the first one's first 32 tokens: two pages of its own column go back for the shared ones
+    for T, L in caches:
+        pos, slots = T.step(torch.tensor([0, 0, 33], device="cuda"), 33)
+        own = T.block_table[2, :2].clone()
+        n = int(T.n_free)
+        T.free_pages[n:n + 2] = own
+        T.n_free += 2
+        T.block_table[2, :2] = T.block_table[0, :2]
+        L.write(slots[32:], pos[32:], k0[32:33], v0[32:33])
+    for step in range(60):
+        q, k, v = (normal(gen, (B, H, hd), "bf16") for _ in range(3))
+        outs = []
+        for i, (T, L) in enumerate(caches):
+            pos, _ = T.step(one, B, 1)
+            outs.append(L.step(pos, q, k, v).clone())
+            if i == 0:  # give back what every later query is past; shared pages with their last holder
+                table, n = T.block_table.cpu().numpy(), int(T.n_free)
+                for b, p in enumerate(pos.tolist()):
+                    for c in range(max(0, p + 1 - W + 1) // ps):
+                        page = int(table[b, c])
+                        if page >= 0:
+                            T.block_table[b, c] = table[b, c] = -1
+                            if not (table[:, :16] == page).any():
+                                T.free_pages[n] = page
+                                n += 1
+                T.n_free.fill_(n)
+                held = [int(x) for b in range(B) for x in table[b, :-(-int(T.lengths[b]) // ps)] if x >= 0]
+                assert sorted(set(held) | set(T.free_pages[:n].tolist())) == list(range(pool))
+                assert len(set(held)) + n == pool
+        assert torch.isfinite(outs[0]).all() and torch.equal(*outs), step
+    T, L = caches[0]
+    T.step(-one, 0)
+    torch.cuda.synchronize()
+    assert int(T.n_free) == pool and sorted(T.free_pages.tolist()) == list(range(pool))
+    T, L = caches[1]  # keeps every page: the shared columns are taken out by hand before the end
+    T.block_table[2, :2] = -1
+    T.step(-one, 0)
+    torch.cuda.synchronize()
+    assert int(T.n_free) == pool and sorted(T.free_pages.tolist()) == list(range(pool))
+    assert mg.maglev_device_status() == 0
+
+
 def test_step_captured_in_a_graph_runs_on():
     """A whole serving step (tables in place, two layers) in one graph: replays continue the sequences by a token each,
     as separate calls do."""
